@@ -359,6 +359,143 @@ int fh_adaln_modulation(const uint16_t* temb_dev, int64_t bt, int64_t d, const u
                         const uint16_t* proj_dev, const uint16_t* bias_dev, int64_t blocks, int64_t n,
                         float* code_dev, float* mod_dev, fh_stream_t stream);
 
+/* Paged NVFP4 key/value cache of one attention layer.  The pages quantize the
+ * query and the key for the score computation (FastH3 Trim, "How fast it runs")
+ * and run the transformer's layers in NVFP4 (FastH3 thread digest, tweet 5/8);
+ * they keep no keys and values between calls.  This library keeps them in its
+ * NVFP4 format, 4.5 bits an element, in pages of page_size tokens:
+ *   k_codes, v_codes    [num_pages, kv_heads, page_size, head_dim / 2] bytes,
+ *                       element 2j of a head in the low nibble of byte j
+ *   k_scales, v_scales  [num_pages, kv_heads, page_size, head_dim / 16] E4M3
+ *   k_gscale, v_gscale  the tensors' FP32 scales, finite and > 0
+ * with k ~ code * scale * k_gscale, and v likewise.  The memory is the
+ * caller's; the struct is read during a call only.  A token's SLOT is
+ * page * page_size + its place in the page.
+ * page_size: a power of two, 16 .. 1024.  head_dim: 64 or 128.  kv_heads:
+ * 1 .. 4096.  num_pages: 0 .. 2^31 - 1, and num_pages * page_size < 2^40.  All
+ * four arrays 16-byte aligned. */
+typedef struct {
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  int64_t num_pages;
+  int64_t page_size;
+  int64_t kv_heads;
+  int64_t head_dim;
+  float k_gscale;
+  float v_gscale;
+} fh_kv_cache;
+
+/* Bits of fh_kv_pages_update's status word. */
+enum {
+  FH_KV_NO_PAGES = 1,        /* the free stack has fewer pages than the requests need */
+  FH_KV_TABLE_FULL = 2,      /* a request needs more than max_pages pages */
+  FH_KV_BAD_LENGTH = 4,      /* a length is negative */
+  FH_KV_STACK_OVERFLOW = 8,  /* more pages given back than the stack holds, or a count < 0 */
+  FH_KV_SLOTS_FULL = 16      /* more new tokens than slot_capacity */
+};
+
+/* Most requests of one fh_kv_pages_update call. */
+#define FH_KV_MAX_BATCH 8192
+
+/* Page bookkeeping of a step, from request lengths on the device.  Request b
+ * holds held[b] cached tokens, in ceil(held[b] / page_size) pages named by the
+ * first entries of row b of block_table, and is to hold target[b]: more for
+ * new tokens, fewer for rejected ones, 0 when it has finished.
+ *   - Pages no longer needed go onto the stack of free pages (free_pages[0 ..
+ *     *free_count - 1], its top last), in the order of the requests and of
+ *     their tables; the entries that named them stay as they are.
+ *   - Then pages needed are taken from its top, in the same order, and entered
+ *     into block_table.
+ *   - lens[b] = target[b]; q_starts[0 .. batch] = the exclusive prefix sum of
+ *     the numbers of new tokens, max(target[b] - held[b], 0), q_starts[batch]
+ *     their total: with lens, what fh_kv_attention takes.
+ *   - slots[q_starts[b] + i] = the slot of request b's token held[b] + i, for
+ *     fh_kv_cache_write; -1 from q_starts[batch] on, up to slot_capacity.
+ *   - *free_count_out = the stack's new count; *status = 0.
+ * All or nothing: if the step cannot be served, *status has the bits that say
+ * why, slots are all -1, q_starts all 0, lens = held, *free_count_out =
+ * *free_count, and block_table and free_pages are as they were.
+ * held, target, lens: int32 [batch]; block_table: int32 [batch, max_pages];
+ * free_pages: int32 [free_capacity]; slots: int64 [slot_capacity]; q_starts:
+ * int32 [batch + 1]; free_count, free_count_out, status: int32, one each; all
+ * device memory.  lens may be held or target, and free_count_out free_count;
+ * other buffers must not overlap.  Called again with the same inputs (counts
+ * and lengths kept apart) it writes the same values again.
+ * 0 <= batch <= FH_KV_MAX_BATCH (0 enqueues nothing); page_size a power of two,
+ * 1 .. 2^20; 0 < max_pages, max_pages * page_size < 2^31; 0 < free_capacity and
+ * 0 <= slot_capacity, both < 2^31.  Results are deterministic. */
+int fh_kv_pages_update(const int32_t* held_dev, const int32_t* target_dev, int64_t batch, int64_t page_size,
+                       int32_t* block_table_dev, int64_t max_pages, int32_t* free_pages_dev, int64_t free_capacity,
+                       const int32_t* free_count_dev, int32_t* free_count_out_dev, int32_t* lens_dev,
+                       int32_t* q_starts_dev, int64_t* slots_dev, int64_t slot_capacity, int32_t* status_dev,
+                       fh_stream_t stream);
+
+/* Quantize new tokens' keys and values into the cache: k and v BF16 [tokens,
+ * kv_heads, head_dim], tokens ldk and ldv elements apart (slices of the fused
+ * QKV projection's rows, say), token i into slots[i] (int64).  Every block of 16
+ * elements of a head is quantized exactly as fh_quantize_act quantizes a row's,
+ * with k_gscale and v_gscale; elements beyond 2688 times the scale are counted
+ * in *clip_count (incremented; may be NULL).  Tokens whose slot is negative or
+ * beyond the cache are left out.  Slots of one call must be distinct: a slot
+ * that two tokens share ends with parts of either.
+ * ldk, ldv >= kv_heads * head_dim, multiples of 8; k, v 16-byte aligned, slots
+ * 8-byte.  tokens >= 0 (0 enqueues nothing). */
+int fh_kv_cache_write(const fh_kv_cache* cache, const uint16_t* k_dev, const uint16_t* v_dev, int64_t tokens,
+                      int64_t ldk, int64_t ldv, const int64_t* slots_dev, unsigned long long* clip_count_dev,
+                      fh_stream_t stream);
+
+/* The cached values of `tokens` slots as BF16, bf16((code * scale) * s_g) in
+ * FP32: k and v [tokens, kv_heads, head_dim], tokens ldk and ldv elements apart.
+ * Rows whose slot is negative or beyond the cache are left as they were.
+ * Alignment and sizes as for fh_kv_cache_write. */
+int fh_kv_cache_read(const fh_kv_cache* cache, const int64_t* slots_dev, int64_t tokens, uint16_t* k_dev,
+                     uint16_t* v_dev, int64_t ldk, int64_t ldv, fh_stream_t stream);
+
+/* Attention of ragged requests over the cache:
+ *   out[t, h] = sum_j p[j] v[j, h / G],
+ *   p = softmax over j of sm_scale * (q[t, h] . k[j, h / G]),  G = q_heads / kv_heads.
+ * Request b has the query rows q_starts[b] .. q_starts[b + 1] - 1 and lens[b]
+ * cached tokens, found through row b of block_table; its queries are its last
+ * tokens: query i stands at position lens[b] - n + i of n.  It sees the cached
+ * tokens j < lens[b] with, if causal, j <= its position and, if window > 0,
+ * j > its position - window.  A query that sees nothing gets out = 0 and
+ * lse = -inf.  lse (FP32 [total_q, q_heads], may be NULL) is the natural
+ * logarithm of the softmax's denominator.
+ * q, out: BF16 [total_q, q_heads, head_dim], tokens ldq and ldo elements apart
+ * (out must not overlap q).  lens int32 [batch], q_starts int32 [batch + 1],
+ * block_table int32 [batch, max_pages]; rows of out and lse that no request has
+ * are left as they were.  What the device arrays hold is brought into range, so
+ * it cannot lead outside a buffer: a table entry that names no page of the
+ * cache leaves its tokens out as a mask would, lengths are cut to max_pages *
+ * page_size, and rows to total_q.
+ * max_q and max_kv are the caller's upper bounds of a request's queries and of
+ * lens (total_q and max_pages * page_size will do): they choose the kernel and
+ * its grid; with wrong ones the call is slower, never wrong.
+ * Scores, maxima, sums and outputs are FP32; the products' operands are FP16:
+ * code * scale is exact there, so is a BF16 query row scaled by a power of two,
+ * and probabilities are rounded to 2^-11.  Deterministic for given arguments
+ * and lengths.
+ * workspace: fh_kv_attention_workspace_bytes(...) bytes of device memory, 16-byte
+ * aligned, zero before the first call that uses it (cudaMemsetAsync); every call
+ * leaves its counters zero again.  Calls that may overlap on the GPU need
+ * workspaces of their own.
+ * q_heads a multiple of kv_heads, total_q * q_heads < 2^31; ldq, ldo >= q_heads *
+ * head_dim, multiples of 8; q, out 16-byte aligned; sm_scale finite; 0 <= window
+ * < 2^31; 0 < max_pages, max_pages * page_size < 2^31.  total_q == 0 or
+ * batch == 0 enqueues nothing. */
+int fh_kv_attention(const fh_kv_cache* cache, const uint16_t* q_dev, int64_t total_q, int64_t q_heads, int64_t ldq,
+                    const int32_t* block_table_dev, int64_t max_pages, const int32_t* lens_dev,
+                    const int32_t* q_starts_dev, int64_t batch, float sm_scale, int causal, int64_t window,
+                    int64_t max_q, int64_t max_kv, uint16_t* out_dev, int64_t ldo, float* lse_dev,
+                    void* workspace_dev, size_t workspace_bytes, fh_stream_t stream);
+
+/* Bytes of workspace that fh_kv_attention needs for these sizes; 0 if they are
+ * not supported. */
+size_t fh_kv_attention_workspace_bytes(int64_t total_q, int64_t batch, int64_t q_heads, int64_t kv_heads,
+                                       int64_t head_dim);
+
 /* Diagnostic of the failure path: enqueues a one-thread kernel whose bounded
  * mbarrier wait (the same wait every pipeline stage of fh_nvfp4_linear uses)
  * can never be satisfied and gives up after limit_us microseconds (1 .. 2e6),

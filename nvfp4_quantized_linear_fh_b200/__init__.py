@@ -32,6 +32,14 @@ FH_ERR_NO_DEVICE = 5
 FH_SCALES_ROWMAJOR = 0
 FH_SCALES_MMA_TILED = 1
 
+# Bits of fh_kv_pages_update's status word.
+FH_KV_NO_PAGES = 1
+FH_KV_TABLE_FULL = 2
+FH_KV_BAD_LENGTH = 4
+FH_KV_STACK_OVERFLOW = 8
+FH_KV_SLOTS_FULL = 16
+FH_KV_MAX_BATCH = 8192
+
 
 class FHError(RuntimeError):
     def __init__(self, status: int, message: str):
@@ -71,6 +79,12 @@ _SIG = {
     "fh_quantize_int8_rows": (_c.c_int, [_P, _I64, _I64, _I64, _P, _P, _P]),
     "fh_int8_attention_scores": (_c.c_int, [_P, _P, _P, _P, _c.c_float, _P, _I64, _I64, _I64, _I64, _P]),
     "fh_adaln_modulation": (_c.c_int, [_P, _I64, _I64, _P, _I64, _P, _P, _I64, _I64, _P, _P, _P]),
+    "fh_kv_pages_update": (_c.c_int, [_P, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _P, _P]),
+    "fh_kv_cache_write": (_c.c_int, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _P]),
+    "fh_kv_cache_read": (_c.c_int, [_P, _P, _I64, _P, _P, _I64, _I64, _P]),
+    "fh_kv_attention": (_c.c_int, [_P, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _c.c_float, _c.c_int, _I64,
+                                   _I64, _I64, _P, _I64, _P, _P, _c.c_size_t, _P]),
+    "fh_kv_attention_workspace_bytes": (_c.c_size_t, [_I64, _I64, _I64, _I64, _I64]),
     "fh_device_status": (_c.c_int, [_P]),
     "fh_selftest_mma_rate": (_c.c_int, [_c.c_int32, _c.c_int32, _c.POINTER(_c.c_int32), _P]),
     "fh_selftest_bounded_wait": (_c.c_int, [_c.c_uint32, _P]),
@@ -422,6 +436,187 @@ def fh_adaln_modulation(temb: torch.Tensor, basis: torch.Tensor, proj: torch.Ten
                          "code [bt, r], mod [blocks, bt, n]")
     _check(_lib.fh_adaln_modulation(_ptr(temb), bt, d, _ptr(basis), r, _ptr(proj), _ptr(bias), blocks, n,
                                     _ptr(code), _ptr(mod), _stream(stream)))
+
+
+# --- the paged NVFP4 key/value cache -------------------------------------------------
+
+class _CKVCache(_c.Structure):
+    """fh_kv_cache of include/fh.h."""
+    _fields_ = [("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P), ("num_pages", _I64),
+                ("page_size", _I64), ("kv_heads", _I64), ("head_dim", _I64), ("k_gscale", _c.c_float),
+                ("v_gscale", _c.c_float)]
+
+
+class KVCache:
+    """One attention layer's keys and values in pages of NVFP4 tokens (fh_kv_cache in include/fh.h): uint8 codes
+    [pages, kv_heads, page_size, head_dim / 2] and E4M3 scales [pages, kv_heads, page_size, head_dim / 16] of each,
+    contiguous on one device, and their FP32 scales.  Holds the tensors; empty_kv_cache makes new ones."""
+
+    def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
+                 k_gscale: float, v_gscale: float):
+        shape = None
+        for t, n, per in ((k_codes, "k_codes", 2), (k_scales, "k_scales", 16), (v_codes, "v_codes", 2),
+                          (v_scales, "v_scales", 16)):
+            _need(t, _U8, n, 4)
+            s = (*t.shape[:3], t.shape[3] * per)
+            if (shape is not None and s != shape) or not t.is_contiguous() or t.device != k_codes.device:
+                raise ValueError("k_codes and v_codes [pages, kv_heads, page_size, head_dim / 2], k_scales and "
+                                 "v_scales [pages, kv_heads, page_size, head_dim / 16], contiguous on one device")
+            shape = s
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = shape
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.k_gscale, self.v_gscale = float(k_gscale), float(v_gscale)
+        self.device = k_codes.device
+        self._c = _CKVCache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+                            self.num_pages, self.page_size, self.kv_heads, self.head_dim, self.k_gscale,
+                            self.v_gscale)
+        self._ref = _P(_c.addressof(self._c))
+
+
+def empty_kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, k_gscale: float, v_gscale: float,
+                   device="cuda") -> KVCache:
+    """A cache of num_pages uninitialised pages."""
+    def new(per):
+        return torch.empty((num_pages, kv_heads, page_size, head_dim // per), dtype=torch.uint8, device=device)
+    return KVCache(new(2), new(16), new(2), new(16), k_gscale, v_gscale)
+
+
+def _need_all(device, dtype, **tensors):
+    """Contiguous tensors of one dtype on `device`, which is the current one: the library launches there."""
+    for n, t in tensors.items():
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+            raise TypeError(f"{n} must be a tensor of {dtype}")
+        if t.device != device:
+            raise ValueError(f"{n} must be on {device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+
+
+def _need_current(device):
+    if device.type != "cuda":
+        raise TypeError("tensors must be CUDA tensors")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, which is not the current device")
+
+
+def fh_kv_pages_update(held: torch.Tensor, target: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+                       free_count: torch.Tensor, free_count_out: torch.Tensor, lens: torch.Tensor,
+                       q_starts: torch.Tensor, slots: torch.Tensor, status: torch.Tensor, page_size: int,
+                       stream=None) -> None:
+    """Block tables, free stack, lens, q_starts and slots of a step in which request b goes from held[b] to target[b]
+    cached tokens (see include/fh.h).  int32: held, target, lens [batch], block_table [batch, max_pages], free_pages
+    [capacity], q_starts [batch + 1], free_count, free_count_out, status [1]; int64 slots.  lens may be held or
+    target, free_count_out may be free_count."""
+    if not isinstance(held, torch.Tensor):
+        raise TypeError("held must be a tensor")
+    device = held.device
+    _need_current(device)
+    _need_all(device, torch.int32, held=held, target=target, block_table=block_table, free_pages=free_pages,
+              free_count=free_count, free_count_out=free_count_out, lens=lens, q_starts=q_starts, status=status)
+    _need_all(device, torch.int64, slots=slots)
+    n = held.numel()
+    if (target.numel() != n or lens.numel() != n or q_starts.numel() != n + 1 or block_table.dim() != 2
+            or block_table.shape[0] != n or free_count.numel() != 1 or free_count_out.numel() != 1
+            or status.numel() != 1):
+        raise ValueError("shape mismatch: held, target, lens [batch], q_starts [batch + 1], block_table [batch, "
+                         "max_pages], free_count, free_count_out, status [1]")
+    _check(_lib.fh_kv_pages_update(held.data_ptr(), target.data_ptr(), n, page_size, block_table.data_ptr(),
+                                   block_table.shape[1], free_pages.data_ptr(), free_pages.numel(),
+                                   free_count.data_ptr(), free_count_out.data_ptr(), lens.data_ptr(),
+                                   q_starts.data_ptr(), slots.data_ptr(), slots.numel(), status.data_ptr(),
+                                   _stream(stream)))
+
+
+def _kv_rows(cache, t, tokens, what):
+    """The token stride of BF16 rows [tokens, kv_heads, head_dim] of the cache's heads."""
+    _need(t, _BF16, what, 3)
+    if t.device != cache.device:
+        raise ValueError(f"{what} must be on {cache.device}")
+    if t.shape != (tokens, cache.kv_heads, cache.head_dim):
+        raise ValueError(f"{what} must have the shape [tokens, kv_heads, head_dim] of slots and cache")
+    return _row_stride(t, what)
+
+
+def _row_stride(t, what):
+    """The token stride of [tokens, heads, d] rows, whose heads must lie one after the other."""
+    tokens, heads, d = t.shape
+    s = t.stride()
+    if (s[2] != 1 and d > 1) or (s[1] != d and heads > 1):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    return s[0] if tokens > 1 else heads * d
+
+
+def fh_kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                      clip_count: torch.Tensor | None = None, stream=None) -> None:
+    """Quantize BF16 k, v [tokens, kv_heads, head_dim] (any token stride) into the cache's slots (int64 [tokens];
+    negative: left out; distinct); clip_count (int64, 1 element) += elements beyond the scales' range."""
+    _need_current(cache.device)
+    _need_all(cache.device, torch.int64, slots=slots)
+    n = slots.numel()
+    ldk, ldv = _kv_rows(cache, k, n, "k"), _kv_rows(cache, v, n, "v")
+    if clip_count is not None:
+        _need_all(cache.device, torch.int64, clip_count=clip_count)
+        if clip_count.numel() < 1:
+            raise ValueError("clip_count must have an element")
+    _check(_lib.fh_kv_cache_write(cache._ref, k.data_ptr(), v.data_ptr(), n, ldk, ldv, slots.data_ptr(),
+                                  None if clip_count is None else clip_count.data_ptr(), _stream(stream)))
+
+
+def fh_kv_cache_read(cache: KVCache, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
+    """BF16 k, v [tokens, kv_heads, head_dim] = the cached values of slots (int64 [tokens]; rows of negative ones are
+    left as they were)."""
+    _need_current(cache.device)
+    _need_all(cache.device, torch.int64, slots=slots)
+    n = slots.numel()
+    ldk, ldv = _kv_rows(cache, k, n, "k"), _kv_rows(cache, v, n, "v")
+    _check(_lib.fh_kv_cache_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), ldk, ldv,
+                                 _stream(stream)))
+
+
+def fh_kv_attention_workspace_bytes(total_q: int, batch: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return _lib.fh_kv_attention_workspace_bytes(total_q, batch, q_heads, kv_heads, head_dim)
+
+
+def empty_kv_attention_workspace(total_q: int, batch: int, q_heads: int, kv_heads: int, head_dim: int,
+                                 device="cuda") -> torch.Tensor:
+    """A zeroed workspace for fh_kv_attention of at most these sizes (each call leaves its counters zero again)."""
+    need = fh_kv_attention_workspace_bytes(total_q, batch, q_heads, kv_heads, head_dim)
+    if need == 0:
+        raise ValueError("sizes that fh_kv_attention does not support")
+    return torch.zeros(need, dtype=torch.uint8, device=device)
+
+
+def fh_kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, lens: torch.Tensor,
+                    q_starts: torch.Tensor, sm_scale: float, out: torch.Tensor, workspace: torch.Tensor, *,
+                    causal: bool = True, window: int = 0, max_q: int | None = None, max_kv: int | None = None,
+                    lse: torch.Tensor | None = None, stream=None) -> None:
+    """out [total_q, q_heads, head_dim] = attention of BF16 q (same shape; any token strides) over the cache, for
+    requests with query rows q_starts[b] .. q_starts[b + 1] - 1 and lens[b] cached tokens in the pages of block_table
+    [batch, max_pages] (int32 all; see include/fh.h).  workspace: empty_kv_attention_workspace(...).  max_q, max_kv:
+    upper bounds of a request's queries and cached tokens, which choose the kernel.  lse: FP32 [total_q, q_heads]."""
+    device = cache.device
+    _need_current(device)
+    _need(q, _BF16, "q", 3)
+    _need(out, _BF16, "out", 3)
+    _need_all(device, torch.int32, block_table=block_table, lens=lens, q_starts=q_starts)
+    _need_all(device, torch.uint8, workspace=workspace)
+    total_q, heads, d = q.shape
+    n = lens.numel()
+    if (d != cache.head_dim or out.shape != q.shape or q.device != device or out.device != device
+            or q_starts.numel() != n + 1 or block_table.dim() != 2 or block_table.shape[0] != n):
+        raise ValueError("shape mismatch: q, out [total_q, q_heads, head_dim], lens [batch], q_starts [batch + 1], "
+                         "block_table [batch, max_pages], on the cache's device")
+    if lse is not None:
+        _need_all(device, torch.float32, lse=lse)
+        if lse.shape != (total_q, heads):
+            raise ValueError("lse must be [total_q, q_heads]")
+    max_pages = block_table.shape[1]
+    _check(_lib.fh_kv_attention(cache._ref, q.data_ptr(), total_q, heads, _row_stride(q, "q"), block_table.data_ptr(),
+                                max_pages, lens.data_ptr(), q_starts.data_ptr(), n, sm_scale, 1 if causal else 0,
+                                window, total_q if max_q is None else max_q,
+                                max_pages * cache.page_size if max_kv is None else max_kv, out.data_ptr(),
+                                _row_stride(out, "out"), None if lse is None else lse.data_ptr(),
+                                workspace.data_ptr(), workspace.numel(), _stream(stream)))
 
 
 def fh_selftest_bounded_wait(limit_us: int, stream=None) -> None:

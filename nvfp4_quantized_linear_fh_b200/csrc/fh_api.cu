@@ -438,6 +438,161 @@ int fh_selftest_mma_rate(int32_t iters, int32_t with_scale_copies, int32_t* pair
   return FH_OK;
 }
 
+// ---- the paged NVFP4 key/value cache -------------------------------------------
+
+static bool pow2_between(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi && (v & (v - 1)) == 0; }
+
+// The checks that every call on a cache makes.  FH_OK, or the failure.
+static int check_kv_cache(const fh_kv_cache* c, const char* who) {
+  if (c == nullptr) return fail(FH_ERR_INVALID_ARG, "%s: null cache", who);
+  if (!(c->k_gscale > 0.0f) || isinf(c->k_gscale) || !(c->v_gscale > 0.0f) || isinf(c->v_gscale))
+    return fail(FH_ERR_INVALID_ARG, "%s: the cache's scales must be finite and > 0", who);
+  if (!pow2_between(c->page_size, 16, 1024) || (c->head_dim != 64 && c->head_dim != 128) || c->kv_heads < 1 ||
+      c->kv_heads > 4096 || c->num_pages < 0 || c->num_pages > 0x7FFFFFFF ||
+      c->num_pages * c->page_size >= ((int64_t)1 << 40))
+    return fail(FH_ERR_UNSUPPORTED_SHAPE,
+                "%s: need page_size a power of two 16 .. 1024, head_dim 64 or 128, 1 <= kv_heads <= 4096, "
+                "0 <= num_pages < 2^31, num_pages * page_size < 2^40",
+                who);
+  if (c->num_pages == 0) return FH_OK;
+  if (c->k_codes == nullptr || c->k_scales == nullptr || c->v_codes == nullptr || c->v_scales == nullptr)
+    return fail(FH_ERR_INVALID_ARG, "%s: null pointer in the cache", who);
+  if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) || !aligned16(c->v_scales))
+    return fail(FH_ERR_UNSUPPORTED_SHAPE, "%s: the cache's arrays must be 16-byte aligned", who);
+  return FH_OK;
+}
+
+static bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int fh_kv_pages_update(const int32_t* held_dev, const int32_t* target_dev, int64_t batch, int64_t page_size,
+                       int32_t* block_table_dev, int64_t max_pages, int32_t* free_pages_dev, int64_t free_capacity,
+                       const int32_t* free_count_dev, int32_t* free_count_out_dev, int32_t* lens_dev,
+                       int32_t* q_starts_dev, int64_t* slots_dev, int64_t slot_capacity, int32_t* status_dev,
+                       fh_stream_t stream) {
+  g_last_error[0] = 0;
+  if (batch < 0 || batch > FH_KV_MAX_BATCH || !pow2_between(page_size, 1, 1 << 20) || max_pages <= 0 ||
+      max_pages > 0x7FFFFFFF / page_size || free_capacity <= 0 || free_capacity > 0x7FFFFFFF || slot_capacity < 0 ||
+      slot_capacity > 0x7FFFFFFF)
+    return fail(FH_ERR_UNSUPPORTED_SHAPE,
+                "fh_kv_pages_update: need 0 <= batch <= 8192, page_size a power of two <= 2^20, max_pages > 0, "
+                "max_pages * page_size < 2^31, 0 < free_capacity < 2^31, 0 <= slot_capacity < 2^31%s");
+  if (batch == 0) return FH_OK;
+  if (held_dev == nullptr || target_dev == nullptr || block_table_dev == nullptr || free_pages_dev == nullptr ||
+      free_count_dev == nullptr || free_count_out_dev == nullptr || lens_dev == nullptr || q_starts_dev == nullptr ||
+      status_dev == nullptr || (slots_dev == nullptr && slot_capacity > 0))
+    return fail(FH_ERR_INVALID_ARG, "fh_kv_pages_update: null pointer%s");
+  for (const void* p : {(const void*)held_dev, (const void*)target_dev, (const void*)block_table_dev,
+                        (const void*)free_pages_dev, (const void*)free_count_dev, (const void*)free_count_out_dev,
+                        (const void*)lens_dev, (const void*)q_starts_dev, (const void*)status_dev})
+    if (!aligned_to(p, 4)) return fail(FH_ERR_UNSUPPORTED_SHAPE, "fh_kv_pages_update: int32 pointers must be aligned%s");
+  if (!aligned_to(slots_dev, 8)) return fail(FH_ERR_UNSUPPORTED_SHAPE, "fh_kv_pages_update: slots must be 8-byte aligned%s");
+  if (int st = check_device()) return st;
+  cudaError_t e = fh::launch_kv_pages(held_dev, target_dev, batch, page_size, block_table_dev, max_pages,
+                                      free_pages_dev, free_capacity, free_count_dev, free_count_out_dev, lens_dev,
+                                      q_starts_dev, slots_dev, slot_capacity, status_dev, (cudaStream_t)stream);
+  return e == cudaSuccess ? FH_OK : cuda_fail(e, "fh_kv_pages_update launch");
+}
+
+// The rows of keys and values of fh_kv_cache_write and fh_kv_cache_read.
+static int check_kv_rows(const fh_kv_cache* c, const void* k, const void* v, int64_t tokens, int64_t ldk, int64_t ldv,
+                         const int64_t* slots, const char* who) {
+  if (int st = check_kv_cache(c, who)) return st;
+  const int64_t row = c->kv_heads * c->head_dim;
+  if (tokens < 0 || tokens > ((int64_t)1 << 40) || ldk < row || ldv < row || ldk % 8 != 0 || ldv % 8 != 0)
+    return fail(FH_ERR_UNSUPPORTED_SHAPE,
+                "%s: need 0 <= tokens <= 2^40, ldk and ldv >= kv_heads * head_dim and multiples of 8", who);
+  if (tokens == 0) return FH_OK;
+  if (k == nullptr || v == nullptr || slots == nullptr) return fail(FH_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned16(k) || !aligned16(v) || !aligned_to(slots, 8))
+    return fail(FH_ERR_UNSUPPORTED_SHAPE, "%s: k and v must be 16-byte aligned, slots 8-byte", who);
+  return FH_OK;
+}
+
+int fh_kv_cache_write(const fh_kv_cache* cache, const uint16_t* k_dev, const uint16_t* v_dev, int64_t tokens,
+                      int64_t ldk, int64_t ldv, const int64_t* slots_dev, unsigned long long* clip_count_dev,
+                      fh_stream_t stream) {
+  g_last_error[0] = 0;
+  if (int st = check_kv_rows(cache, k_dev, v_dev, tokens, ldk, ldv, slots_dev, "fh_kv_cache_write")) return st;
+  if (!aligned_to(clip_count_dev, 8))
+    return fail(FH_ERR_UNSUPPORTED_SHAPE, "fh_kv_cache_write: clip_count must be 8-byte aligned%s");
+  if (tokens == 0 || cache->num_pages == 0) return FH_OK;
+  if (int st = check_device()) return st;
+  cudaError_t e = fh::launch_kv_write(*cache, k_dev, v_dev, tokens, ldk, ldv, slots_dev, clip_count_dev,
+                                      (cudaStream_t)stream);
+  return e == cudaSuccess ? FH_OK : cuda_fail(e, "fh_kv_cache_write launch");
+}
+
+int fh_kv_cache_read(const fh_kv_cache* cache, const int64_t* slots_dev, int64_t tokens, uint16_t* k_dev,
+                     uint16_t* v_dev, int64_t ldk, int64_t ldv, fh_stream_t stream) {
+  g_last_error[0] = 0;
+  if (int st = check_kv_rows(cache, k_dev, v_dev, tokens, ldk, ldv, slots_dev, "fh_kv_cache_read")) return st;
+  if (tokens == 0 || cache->num_pages == 0) return FH_OK;
+  if (int st = check_device()) return st;
+  cudaError_t e = fh::launch_kv_read(*cache, slots_dev, tokens, k_dev, v_dev, ldk, ldv, (cudaStream_t)stream);
+  return e == cudaSuccess ? FH_OK : cuda_fail(e, "fh_kv_cache_read launch");
+}
+
+static bool kv_attention_sizes(int64_t total_q, int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+  return total_q >= 0 && batch >= 0 && batch <= 0x7FFFFFFF - 1 && kv_heads >= 1 && kv_heads <= 4096 && q_heads >= kv_heads &&
+         q_heads <= 0x7FFFFFFF && q_heads % kv_heads == 0 && (head_dim == 64 || head_dim == 128) &&
+         total_q <= 0x7FFFFFFF / q_heads;
+}
+
+size_t fh_kv_attention_workspace_bytes(int64_t total_q, int64_t batch, int64_t q_heads, int64_t kv_heads,
+                                       int64_t head_dim) {
+  if (!kv_attention_sizes(total_q, batch, q_heads, kv_heads, head_dim)) return 0;
+  return fh::kv_attention_workspace(fh::KvAttnShape{total_q, batch, q_heads, kv_heads, head_dim, 0, 0});
+}
+
+int fh_kv_attention(const fh_kv_cache* cache, const uint16_t* q_dev, int64_t total_q, int64_t q_heads, int64_t ldq,
+                    const int32_t* block_table_dev, int64_t max_pages, const int32_t* lens_dev,
+                    const int32_t* q_starts_dev, int64_t batch, float sm_scale, int causal, int64_t window,
+                    int64_t max_q, int64_t max_kv, uint16_t* out_dev, int64_t ldo, float* lse_dev,
+                    void* workspace_dev, size_t workspace_bytes, fh_stream_t stream) {
+  g_last_error[0] = 0;
+  if (int st = check_kv_cache(cache, "fh_kv_attention")) return st;
+  if (!isfinite(sm_scale)) return fail(FH_ERR_INVALID_ARG, "fh_kv_attention: sm_scale must be finite%s");
+  if (!kv_attention_sizes(total_q, batch, q_heads, cache->kv_heads, cache->head_dim))
+    return fail(FH_ERR_UNSUPPORTED_SHAPE,
+                "fh_kv_attention: need q_heads a multiple of kv_heads, total_q * q_heads < 2^31, batch >= 0%s");
+  const int64_t row = q_heads * cache->head_dim;
+  if (ldq < row || ldo < row || ldq % 8 != 0 || ldo % 8 != 0 || max_pages <= 0 ||
+      max_pages > 0x7FFFFFFF / cache->page_size || window < 0 || window > 0x7FFFFFFF || max_q < 0 || max_kv < 0)
+    return fail(FH_ERR_UNSUPPORTED_SHAPE,
+                "fh_kv_attention: need ldq and ldo >= q_heads * head_dim and multiples of 8, max_pages > 0, "
+                "max_pages * page_size < 2^31, 0 <= window < 2^31, max_q and max_kv >= 0%s");
+  if (total_q == 0 || batch == 0) return FH_OK;
+  if (q_dev == nullptr || block_table_dev == nullptr || lens_dev == nullptr || q_starts_dev == nullptr ||
+      out_dev == nullptr || workspace_dev == nullptr)
+    return fail(FH_ERR_INVALID_ARG, "fh_kv_attention: null pointer%s");
+  if (!aligned16(q_dev) || !aligned16(out_dev) || !aligned16(workspace_dev) || !aligned_to(block_table_dev, 4) ||
+      !aligned_to(lens_dev, 4) || !aligned_to(q_starts_dev, 4) || !aligned_to(lse_dev, 4))
+    return fail(FH_ERR_UNSUPPORTED_SHAPE,
+                "fh_kv_attention: q, out and workspace must be 16-byte aligned, the other arrays 4-byte%s");
+  const int64_t most_kv = max_pages * cache->page_size;
+  fh::KvAttnShape shape{total_q, batch, q_heads, cache->kv_heads, cache->head_dim, max_q < total_q ? max_q : total_q,
+                        max_kv < most_kv ? max_kv : most_kv};
+  if (shape.max_q < 1) shape.max_q = 1;
+  if (workspace_bytes < fh::kv_attention_workspace(shape))
+    return fail(FH_ERR_INVALID_ARG, "fh_kv_attention: workspace too small%s");
+  if (int st = check_device()) return st;
+  fh::KvAttnCall call;
+  call.q = q_dev;
+  call.out = out_dev;
+  call.lse = lse_dev;
+  call.table = block_table_dev;
+  call.lens = lens_dev;
+  call.q_starts = q_starts_dev;
+  call.ldq = ldq;
+  call.ldo = ldo;
+  call.max_pages = max_pages;
+  call.sm_scale = sm_scale;
+  call.causal = causal != 0;
+  call.window = (int)window;
+  cudaError_t e = fh::launch_kv_attention(*cache, call, shape, workspace_dev, (cudaStream_t)stream);
+  return e == cudaSuccess ? FH_OK : cuda_fail(e, "fh_kv_attention launch");
+}
+
 int fh_device_status(fh_stream_t stream) {
   g_last_error[0] = 0;
   if (int st = check_device()) return st;

@@ -134,6 +134,39 @@ cudaError_t launch_adaln_modulation(const uint16_t* e, int64_t bt, int64_t d, co
                                     const uint16_t* proj, const uint16_t* bias, int64_t L, int64_t n, float* code,
                                     float* mod, cudaStream_t s);
 
+// The paged NVFP4 key/value cache (fh_kv_pages.cu, fh_kv_cache.cu).  Arguments
+// are validated by the caller.
+cudaError_t launch_kv_pages(const int32_t* held, const int32_t* target, int64_t batch, int64_t page_size,
+                            int32_t* table, int64_t max_pages, int32_t* free_pages, int64_t free_capacity,
+                            const int32_t* free_count, int32_t* free_count_out, int32_t* lens, int32_t* q_starts,
+                            int64_t* slots, int64_t slot_capacity, int32_t* status, cudaStream_t s);
+cudaError_t launch_kv_write(const fh_kv_cache& c, const uint16_t* k, const uint16_t* v, int64_t tokens, int64_t ldk,
+                            int64_t ldv, const int64_t* slots, unsigned long long* clip, cudaStream_t s);
+cudaError_t launch_kv_read(const fh_kv_cache& c, const int64_t* slots, int64_t tokens, uint16_t* k, uint16_t* v,
+                           int64_t ldk, int64_t ldv, cudaStream_t s);
+
+// Attention over the cache (fh_kv_attn.cu and the kernels' own files).  The
+// shape's max_q and max_kv are upper bounds that the host has; results do not
+// depend on them.
+struct KvAttnShape {
+  int64_t total_q, batch, q_heads, kv_heads, head_dim, max_q, max_kv;
+};
+struct KvAttnCall {
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* q_starts;
+  int64_t ldq, ldo, max_pages;
+  float sm_scale;
+  bool causal;
+  int window;
+};
+size_t kv_attention_workspace(const KvAttnShape& s);
+cudaError_t launch_kv_attention(const fh_kv_cache& c, const KvAttnCall& call, const KvAttnShape& shape,
+                                void* workspace, cudaStream_t s);
+
 // The layer on host buffers, pipelined over row chunks (fh_host.cu).  Arguments
 // are validated by the caller; the workspace holds host_linear_workspace_bytes.
 size_t host_linear_workspace_bytes(int64_t K, int64_t N, int64_t chunk_rows);

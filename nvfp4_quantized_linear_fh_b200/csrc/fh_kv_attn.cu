@@ -1,0 +1,45 @@
+// fh_kv_attn.cu -- attention over the paged NVFP4 cache: which kernel takes a call.
+#include <math.h>
+
+#include "fh_internal.h"
+#include "fh_kv_attn.h"
+
+namespace fh {
+
+size_t kv_attention_workspace(const KvAttnShape& s) { return kv_attn_split_workspace(s); }
+
+cudaError_t launch_kv_attention(const fh_kv_cache& c, const KvAttnCall& call, const KvAttnShape& shape,
+                                void* workspace, cudaStream_t s) {
+  kv::AttnParams p;
+  p.q = call.q;
+  p.out = call.out;
+  p.lse = call.lse;
+  p.k_codes = c.k_codes;
+  p.k_scales = c.k_scales;
+  p.v_codes = c.v_codes;
+  p.v_scales = c.v_scales;
+  p.table = call.table;
+  p.lens = call.lens;
+  p.q_starts = call.q_starts;
+  p.ldq = call.ldq;
+  p.ldo = call.ldo;
+  p.max_pages = call.max_pages;
+  p.total_q = (int)shape.total_q;
+  p.batch = (int)shape.batch;
+  p.q_heads = (int)shape.q_heads;
+  p.kv_heads = (int)shape.kv_heads;
+  p.group = (int)(shape.q_heads / shape.kv_heads);
+  p.page_shift = 0;
+  while (((int64_t)1 << p.page_shift) < c.page_size) ++p.page_shift;
+  p.num_pages = (int)c.num_pages;
+  p.causal = call.causal ? 1 : 0;
+  p.window = call.window;
+  p.qk_scale = (float)((double)call.sm_scale * 1.4426950408889634 * (double)c.k_gscale);
+  p.v_gscale = c.v_gscale;
+  p.part_o = nullptr;
+  p.part_ml = nullptr;
+  p.count = nullptr;
+  return launch_kv_attn_split(p, shape, workspace, s);
+}
+
+}  // namespace fh

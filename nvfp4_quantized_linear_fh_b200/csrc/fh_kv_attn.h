@@ -1,0 +1,70 @@
+// fh_kv_attn.h -- what the two attention kernels over the NVFP4 cache share.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fh_internal.h"
+
+namespace fh {
+namespace kv {
+
+struct AttnParams {
+  const uint16_t* q;  // BF16 [total_q, q_heads, d], tokens ldq elements apart
+  uint16_t* out;      // BF16 [total_q, q_heads, d], tokens ldo elements apart
+  float* lse;         // FP32 [total_q, q_heads] or null
+  const uint8_t* k_codes;
+  const uint8_t* k_scales;
+  const uint8_t* v_codes;
+  const uint8_t* v_scales;
+  const int32_t* table;     // [batch, max_pages]
+  const int32_t* lens;      // [batch]
+  const int32_t* q_starts;  // [batch + 1]
+  int64_t ldq, ldo, max_pages;
+  int total_q, batch, q_heads, kv_heads, group;  // group = q_heads / kv_heads
+  int page_shift, num_pages;
+  int causal, window;
+  float qk_scale;  // sm_scale * log2(e) * k_gscale: scores in units of log2
+  float v_gscale;
+  // Workspace: partial results of key ranges split over CTAs, and their counters.
+  float* part_o;        // [slots][rows][d], not normalised
+  float2* part_ml;      // [slots][rows]: running maximum (log2 units) and sum
+  unsigned int* count;  // zero between calls
+};
+
+// One request as every kernel reads it, with the lengths brought into range so
+// that no index built from them leaves a buffer.
+struct Request {
+  int row0, n_q;  // first row of q, and how many
+  int len;        // cached tokens
+  int lo, hi;     // cached tokens that any of its queries may see: [lo, hi)
+};
+
+__device__ __forceinline__ Request load_request(const AttnParams& p, int b) {
+  Request r;
+  const int s = min(max(p.q_starts[b], 0), p.total_q), e = min(max(p.q_starts[b + 1], s), p.total_q);
+  r.row0 = s;
+  r.n_q = e - s;
+  r.len = (int)min((int64_t)max(p.lens[b], 0), p.max_pages << p.page_shift);
+  r.hi = r.len;
+  r.lo = 0;
+  if (p.window > 0) r.lo = (int)min((int64_t)r.hi, max((int64_t)0, (int64_t)r.len - r.n_q - p.window + 1));
+  return r;
+}
+
+// The cached tokens [lo, hi) that query i of a request sees.
+__device__ __forceinline__ int2 seen_by(const AttnParams& p, const Request& r, int i) {
+  const int64_t pos = (int64_t)r.len - r.n_q + i;
+  int2 s = make_int2(0, r.len);
+  if (p.causal) s.y = (int)min((int64_t)r.len, max((int64_t)0, pos + 1));
+  if (p.window > 0) s.x = (int)min((int64_t)s.y, max((int64_t)0, pos - p.window + 1));
+  return s;
+}
+
+}  // namespace kv
+
+// Few rows a request (fh_kv_decode.cu).
+size_t kv_attn_split_workspace(const KvAttnShape& s);
+cudaError_t launch_kv_attn_split(const kv::AttnParams& p, const KvAttnShape& shape, void* workspace, cudaStream_t s);
+
+}  // namespace fh

@@ -41,6 +41,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <new>
+
 #include "fh_internal.h"
 #include "fh_nvfp4.cuh"
 
@@ -192,22 +194,31 @@ void build_table(float sg_f, QuantTable* t) {
 
 }  // namespace
 
-// Small per-thread cache: calibrated layers reuse one s_g for every call.
+// Per-thread cache: calibrated layers reuse one s_g for every call, and a model
+// has a few hundred of them (building a table takes far longer than a launch).
+// 512 places found by a hash of the scale's bits; a scale that meets another one
+// in its place is built anew there.
 const QuantTable& quant_table_for(float sg) {
   struct Entry {
     float sg;
-    bool valid;
     QuantTable t;
   };
-  thread_local Entry cache[4] = {};
-  thread_local int next = 0;
-  for (auto& e : cache)
-    if (e.valid && e.sg == sg) return e.t;
-  Entry& e = cache[next];
-  next = (next + 1) & 3;
+  struct Cache {
+    Entry* at[512] = {};
+    Entry spare;  // when there is no memory for another entry
+    ~Cache() {
+      for (Entry* e : at) delete e;
+    }
+  };
+  thread_local Cache cache;
+  uint32_t bits;
+  memcpy(&bits, &sg, 4);
+  Entry*& place = cache.at[(bits * 0x9E3779B1u) >> 23];
+  if (place != nullptr && place->sg == sg) return place->t;
+  if (place == nullptr) place = new (std::nothrow) Entry;
+  Entry& e = place != nullptr ? *place : cache.spare;
   build_table(sg, &e.t);
   e.sg = sg;
-  e.valid = true;
   return e.t;
 }
 

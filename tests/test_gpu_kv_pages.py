@@ -1,0 +1,141 @@
+"""fh_kv_pages_update against the documented rules, one page after another."""
+import numpy as np
+import pytest
+import torch
+
+from _gpu_util import fh
+from _kv_ref import pages_update
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(a):
+    return torch.tensor(np.asarray(a, dtype=np.int32), device="cuda")
+
+
+def start(rng, n, page, held, spare, width_extra=2, target=None):
+    """A consistent state: every request holds the pages of its tokens, the others are free."""
+    held = np.asarray(held)
+    hp = -(-np.maximum(held, 0) // page)
+    width = int(max(hp.max(initial=0), (-(-np.maximum(target, 0) // page)).max(initial=0))) + width_extra
+    total = int(hp.sum()) + spare
+    order = rng.permutation(total)
+    table = np.full((n, width), -7, np.int64)
+    at = 0
+    for b in range(n):
+        table[b, :hp[b]] = order[at:at + hp[b]]
+        at += hp[b]
+    free = np.full(max(total, 1), -9, np.int64)
+    free[:total - at] = order[at:]
+    return table, free, total - at
+
+
+def run(held, target, table, free, count, page, cap, alias=False):
+    m = fh()
+    n = len(held)
+    d = dict(held=i32(held), target=i32(target), table=i32(table), free=i32(free), count=i32([count]))
+    lens = d["held"] if alias else i32(np.full(n, 77))
+    out = d["count"] if alias else i32([-5])
+    q_starts, status = i32(np.full(n + 1, 77)), i32([99])
+    slots = torch.full((cap + 8,), 12345, dtype=torch.int64, device="cuda")
+    m.fh_kv_pages_update(d["held"], d["target"], d["table"], d["free"], d["count"], out, lens, q_starts, slots[:cap],
+                         status, page)
+    torch.cuda.synchronize()
+    assert (slots[cap:] == 12345).all()
+    return (int(status), d["table"].cpu().numpy(), d["free"].cpu().numpy(), int(out), lens.cpu().numpy(),
+            q_starts.cpu().numpy(), slots[:cap].cpu().numpy())
+
+
+def check(held, target, table, free, count, page, cap, alias=False):
+    ref = pages_update(held, target, table, free, count, page, cap, table.shape[1])
+    got = run(held, target, table, free, count, page, cap, alias)
+    for name, r, g in zip(("status", "table", "free", "count", "lens", "q_starts", "slots"), ref, got):
+        np.testing.assert_array_equal(g, r, err_msg=name)
+    return got
+
+
+def mixed(rng, n, page, most, grow):
+    held = rng.integers(0, most + 1, n)
+    target = held + rng.integers(0, grow + 1, n)
+    kind = rng.integers(0, 6, n)
+    target = np.where(kind == 0, 0, target)
+    target = np.where(kind == 1, rng.integers(0, held + 1), target)
+    return held, target
+
+
+@pytest.mark.parametrize("n,page,most,grow", [(1, 16, 0, 1), (1, 16, 40, 1), (1, 1, 5, 3), (3, 16, 100, 33),
+                                              (33, 32, 500, 1), (256, 16, 700, 5), (1000, 64, 900, 130),
+                                              (1025, 16, 60, 40), (8192, 16, 40, 20), (7, 1024, 5000, 3000)])
+@pytest.mark.parametrize("alias", [False, True])
+def test_mixed_steps(n, page, most, grow, alias):
+    rng = np.random.default_rng(n * 7 + page)
+    held, target = mixed(rng, n, page, most, grow)
+    need = int(np.maximum(-(-target // page) - -(-held // page), 0).sum())
+    table, free, count = start(rng, n, page, held, need + 3, target=target)
+    rows = int(np.maximum(target - held, 0).sum())
+    check(held, target, table, free, count, page, rows + 5, alias)
+
+
+def test_growth_served_by_pages_given_back_in_the_same_step():
+    rng = np.random.default_rng(1)
+    held, target = np.array([100, 5, 64, 0]), np.array([0, 90, 16, 33])
+    table, free, count = start(rng, 4, 16, held, 2, target=target)
+    status, *_ = check(held, target, table, free, count, 16, 200)
+    assert status == 0
+
+
+def test_pool_used_up_exactly_and_one_page_short():
+    rng = np.random.default_rng(2)
+    held, target = np.array([16, 20]), np.array([17, 49])
+    table, free, count = start(rng, 2, 16, held, 3, target=target)
+    assert check(held, target, table, free, count, 16, 64)[0] == 0
+    table, free, count = start(rng, 2, 16, held, 2, target=target)
+    assert check(held, target, table, free, count, 16, 64)[0] == fh().FH_KV_NO_PAGES
+
+
+@pytest.mark.parametrize("alias", [False, True])
+def test_refused_steps_leave_everything_as_it_was(alias):
+    m = fh()
+    rng = np.random.default_rng(3)
+    held, target = np.array([30, 5, 50]), np.array([60, 6, 0])
+    table, free, count = start(rng, 3, 16, held, 8, target=target)
+    assert check(held, target, table, free, count, 16, 30, alias)[0] == m.FH_KV_SLOTS_FULL   # 31 new tokens
+    assert check(held, target, table, free, count, 16, 31, alias)[0] == 0
+    assert check(held, np.array([60, -1, 0]), table, free, count, 16, 64, alias)[0] == m.FH_KV_BAD_LENGTH
+    assert check(np.array([30, -5, 50]), target, table, free, count, 16, 64, alias)[0] == m.FH_KV_BAD_LENGTH
+    assert check(held, np.array([10 ** 9, 6, 0]), table, free, count, 16, 64, alias)[0] & m.FH_KV_TABLE_FULL
+    assert check(held, target, table, free, len(free), 16, 64, alias)[0] == m.FH_KV_STACK_OVERFLOW
+    assert check(held, target, table, free, -1, 16, 64, alias)[0] & m.FH_KV_STACK_OVERFLOW
+    big = np.array([2 ** 31 - 1] * 3)
+    assert check(held, big, table, free, count, 16, 64, alias)[0] & m.FH_KV_TABLE_FULL
+
+
+def test_no_new_tokens_and_no_slots():
+    rng = np.random.default_rng(4)
+    held = np.array([3, 40, 0])
+    table, free, count = start(rng, 3, 16, held, 1, target=held)
+    check(held, held, table, free, count, 16, 0)
+    check(held, held, table, free, count, 16, 300)
+
+
+def test_same_inputs_again_give_the_same():
+    m = fh()
+    rng = np.random.default_rng(5)
+    held, target = mixed(rng, 200, 16, 300, 40)
+    table, free, count = start(rng, 200, 16, held, 4000, target=target)
+    d = [i32(x) for x in (held, target, table, free, [count])]
+    out, lens, qs, status = i32([0]), i32(np.zeros(200)), i32(np.zeros(201)), i32([0])
+    slots = torch.zeros(9000, dtype=torch.int64, device="cuda")
+    seen = []
+    for _ in range(3):
+        m.fh_kv_pages_update(*d, out, lens, qs, slots, status, 16)
+        seen.append([x.clone() for x in (d[2], d[3], out, lens, qs, slots, status)])
+    for a in seen[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(seen[0], a))
+
+
+def test_unknown_page_gives_no_slot():
+    """A table entry below 0 where held tokens end inside a page: their new neighbours get no slot."""
+    table = np.full((1, 4), -1)
+    got = run([5], [20], table, np.array([3, 2, 1]), 3, 16, 20)
+    assert got[0] == 0 and (got[6][:11] == -1).all() and got[6][11:15].tolist() == [16, 17, 18, 19]
