@@ -596,12 +596,13 @@ int fh_kv_attention(const fh_kv_cache* cache, const uint16_t* q_dev, int64_t tot
 int fh_device_status(fh_stream_t stream) {
   g_last_error[0] = 0;
   if (int st = check_device()) return st;
-  unsigned int bits = 0, qbits = 0, ibits = 0;
+  unsigned int bits = 0, qbits = 0, ibits = 0, kbits = 0;
   cudaError_t e = fh::read_and_clear_device_error(&bits, (cudaStream_t)stream);
   if (e == cudaSuccess) e = fh::read_and_clear_quant_error(&qbits);
   if (e == cudaSuccess) e = fh::read_and_clear_int8_error(&ibits);
+  if (e == cudaSuccess) e = fh::read_and_clear_kv_error(&kbits);
   if (e != cudaSuccess) return cuda_fail(e, "fh_device_status");
-  bits |= qbits | ibits;
+  bits |= qbits | ibits | kbits;
   if (bits & fh::kDevErrTimeout)
     return fail(FH_ERR_TIMEOUT, "a kernel gave up on a bounded on-chip wait%s");
   return FH_OK;

@@ -26,6 +26,9 @@ cudaError_t read_and_clear_quant_error(unsigned int* bits);
 // The INT8 score kernel's error word (fh_int8.cu); call after the stream is synchronized.
 cudaError_t read_and_clear_int8_error(unsigned int* bits);
 
+// The cache attention's error word (fh_kv_prefill.cu); call after the stream is synchronized.
+cudaError_t read_and_clear_kv_error(unsigned int* bits);
+
 // Per-device caches of the host side.  Each table holds one int per device
 // ordinal, 0 meaning "not filled yet"; the first call on a device fills its
 // entry with the device current.  Entries are atomics, so host threads may

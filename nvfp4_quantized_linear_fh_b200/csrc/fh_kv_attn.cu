@@ -39,6 +39,7 @@ cudaError_t launch_kv_attention(const fh_kv_cache& c, const KvAttnCall& call, co
   p.part_o = nullptr;
   p.part_ml = nullptr;
   p.count = nullptr;
+  if (shape.max_q * p.group > 16) return launch_kv_attn_tiles(p, shape, s);
   return launch_kv_attn_split(p, shape, workspace, s);
 }
 

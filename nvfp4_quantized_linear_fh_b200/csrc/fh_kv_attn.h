@@ -67,4 +67,7 @@ __device__ __forceinline__ int2 seen_by(const AttnParams& p, const Request& r, i
 size_t kv_attn_split_workspace(const KvAttnShape& s);
 cudaError_t launch_kv_attn_split(const kv::AttnParams& p, const KvAttnShape& shape, void* workspace, cudaStream_t s);
 
+// Tiles of many rows, on the tcgen05 tensor cores (fh_kv_prefill.cu).
+cudaError_t launch_kv_attn_tiles(const kv::AttnParams& p, const KvAttnShape& shape, cudaStream_t s);
+
 }  // namespace fh

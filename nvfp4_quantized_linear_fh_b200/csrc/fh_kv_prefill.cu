@@ -1,0 +1,662 @@
+// fh_kv_prefill.cu -- attention over the paged NVFP4 cache for many query rows a
+// request (prompts, whole clips), on the tcgen05 tensor cores.
+//
+// The same attention as fh_kv_decode.cu; here the two products bound it, and
+// beside them the exponentials: 256 rows x 128 keys take 2048 cycles of a
+// SM's FP16 tensor rate at d = 128, and as many of its 16 exponentials a cycle.
+//
+// A CTA has 256 packed query rows (row = token * G + head in group) of one
+// request and KV head, as two 128-row tiles, and walks 128-token key tiles:
+//   warps 0..3, 4..7   one row a thread, a tile each: scores from TMEM, running
+//                      maximum and sum, P back to TMEM over the scores' columns,
+//                      where the second product takes it as its A operand.
+//   warps 8..11        codes from global memory, converted to code * scale in
+//                      FP16 (exact) and laid out in 128-byte swizzled rows; the
+//                      same layout serves K as a K-major operand and V as an
+//                      MN-major one, so V is not transposed.  The next tile's
+//                      codes are in registers while the current one is stored.
+//   warp 12            issues the products: S = Q K^T of one tile while the other
+//                      tile's softmax runs, O += P V.
+// The output stays in TMEM.  It is rescaled only when a row's maximum grows by
+// more than 8 (in log2), by the row's own thread: the commit that announces
+// S(j) also covers O += P(j-1) V, so nothing else is writing O then.
+//
+// Queries, probabilities, sums and roundings are as in fh_kv_decode.cu.  Every
+// mbarrier wait is bounded; on expiry the kernel sets its error word, drains
+// what it issued, frees its TMEM and returns.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "fh_internal.h"
+#include "fh_kv.cuh"
+#include "fh_kv_attn.h"
+
+namespace fh {
+
+namespace {
+
+using namespace kv;
+
+__device__ unsigned int g_kv_error = 0;
+
+constexpr int kRows = 128;     // query rows of a tile (threads of a softmax group)
+constexpr int kTiles = 2;      // tiles of a CTA
+constexpr int kKeys = 128;     // tokens of a key tile
+constexpr int kStages = 2;     // of K and of V
+constexpr int kSoftWarps = 4 * kTiles;
+constexpr int kFeedWarps = 4;
+constexpr int kMmaWarp = kSoftWarps + kFeedWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kLive = 4;       // ring of the key tiles' page masks
+constexpr float kRaise = 8.0f;
+constexpr float kHead = 6.0f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;                 // 64-element (128-byte) column blocks of an operand
+  static constexpr int kHalfBytes = 128 * 128;           // 128 rows of 128 bytes
+  static constexpr int kOperand = kHalves * kHalfBytes;  // Q tile, K tile, V tile
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + kTiles * kOperand;
+  static constexpr int kOffV = kOffK + kStages * kOperand;
+  static constexpr int kOffBar = kOffV + kStages * kOperand;
+  static constexpr int kBars = 4 * kStages + 3 * kTiles + 2;
+  static constexpr int kOffLive = kOffBar + 8 * kBars;
+  static constexpr int kOffMisc = kOffLive + 8 * kLive;
+  // At least half of an SM's shared memory, so that no two CTAs of an SM wait for each other's TMEM.
+  static constexpr int kNeed = kOffMisc + 64 + 1024;
+  static constexpr int kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
+  static constexpr int kTmemS = 0, kTmemO = kTiles * kKeys;  // column offsets
+  static_assert(kTmemO + kTiles * D <= 512, "TMEM");
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+__device__ __forceinline__ uint32_t s_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
+}
+
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool bar_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+
+// Bounded wait (~4 s, or until another role gave up): sets the error word and
+// the CTA's abort flag on expiry.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (bar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = now_ns();
+  for (uint32_t i = 1; i < (1u << 30); ++i) {
+    if (bar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0u) {
+      if (*abort) return false;
+      if (now_ns() - t0 > 4000000000ull) break;
+    }
+  }
+  atomicOr(&g_kv_error, (unsigned)kDevErrTimeout);
+  *abort = 1;
+  return false;
+}
+
+// The wait of a whole warp: false for all lanes if any gave up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, abort));
+}
+
+// Drain wait: bounded by time only (~1 s), ignores the abort flag.
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
+  if (bar_try_wait(bar, parity)) return;
+  const uint64_t t0 = now_ns();
+  for (uint32_t i = 1; i < (1u << 30); ++i) {
+    if (bar_try_wait(bar, parity)) return;
+    if ((i & 255u) == 0u && now_ns() - t0 > 1000000000ull) break;
+  }
+  atomicOr(&g_kv_error, (unsigned)kDevErrTimeout);
+}
+
+__device__ __forceinline__ bool elect() {
+  uint32_t pred = 0;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(pred));
+  return pred != 0;
+}
+
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Operand descriptors of 128-byte swizzled rows in 1024-byte atoms of eight
+// rows (the stride between atoms down the rows).  lead: for an MN-major
+// operand, the bytes between 64-element column blocks.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lead) {
+  uint64_t dsc = (uint64_t)((addr >> 4) & 0x3FFFu);
+  dsc |= (uint64_t)(lead >> 4) << 16;
+  dsc |= (uint64_t)(1024u >> 4) << 32;
+  dsc |= (uint64_t)1u << 46;
+  dsc |= (uint64_t)2u << 61;
+  return dsc;
+}
+
+// tcgen05.mma kind::f16: FP16 operands, FP32 accumulator; M = 128.
+__host__ __device__ constexpr uint32_t idesc(int n, bool b_mn_major) {
+  return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_load_32(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+        "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+        "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr));
+}
+
+// Completes the tcgen05.ld that wrote v; the registers are tied to the wait so
+// that no use of them can be scheduled before it.
+__device__ __forceinline__ void tmem_wait_32(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                 "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                 "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+                 "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_store_32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32],"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
+      "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_store_16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16],"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// What a CTA works on.
+struct Job {
+  Request rq;
+  int b, head, row0, n_rows;  // packed rows row0 .. row0 + n_rows - 1 of the request
+  int key0, n_keys;           // first key tile, and how many
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_constant__ AttnParams p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t sbase = s_u32(smem);
+  const uint32_t bar0 = sbase + C::kOffBar;
+  auto kfull = [&](int s) { return bar0 + 8u * s; };
+  auto kempty = [&](int s) { return bar0 + 8u * (kStages + s); };
+  auto vfull = [&](int s) { return bar0 + 8u * (2 * kStages + s); };
+  auto vempty = [&](int s) { return bar0 + 8u * (3 * kStages + s); };
+  auto sfull = [&](int t) { return bar0 + 8u * (4 * kStages + t); };            // scores written
+  auto pfull = [&](int t) { return bar0 + 8u * (4 * kStages + kTiles + t); };   // probabilities written
+  auto ofull = [&](int t) { return bar0 + 8u * (4 * kStages + 2 * kTiles + t); };
+  const uint32_t qfull = bar0 + 8u * (4 * kStages + 3 * kTiles);
+  const uint32_t drained = qfull + 8u;
+  uint64_t* live_s = reinterpret_cast<uint64_t*>(smem + C::kOffLive);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
+  int* job_s = reinterpret_cast<int*>(smem + C::kOffMisc + 16);  // request, tile
+  __shared__ int scan_s[kThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // --- which request and rows: the tiles of all requests in one line, the last
+  // (under a causal mask the longest) first, heads next to one another ---------------
+  constexpr int kCtaRows = kRows * kTiles;
+  auto tiles_of = [&](int b) {
+    return (int)(((int64_t)load_request(p, b).n_q * p.group + kCtaRows - 1) / kCtaRows);
+  };
+  const int per = (p.batch + kThreads - 1) / kThreads;
+  const int rb0 = min(p.batch, tid * per), rb1 = min(p.batch, rb0 + per);
+  int mine = 0;
+  for (int b = rb0; b < rb1; ++b) mine += tiles_of(b);
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scan_s[warp] = incl;
+  __syncthreads();
+  int before = incl - mine, total = 0;
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) before += scan_s[i];
+    total += scan_s[i];
+  }
+  const int slot = total - 1 - (int)(blockIdx.x / p.kv_heads);
+  if (slot < 0) return;
+  if (slot >= before && slot < before + mine) {
+    int rest = slot - before;
+    for (int b = rb0; b < rb1; ++b) {
+      const int n = tiles_of(b);
+      if (rest < n) {
+        job_s[0] = b;
+        job_s[1] = rest;
+        break;
+      }
+      rest -= n;
+    }
+  }
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      bar_init(kfull(s), 32 * kFeedWarps);
+      bar_init(kempty(s), 1);
+      bar_init(vfull(s), 32 * kFeedWarps);
+      bar_init(vempty(s), 1);
+    }
+    for (int t = 0; t < kTiles; ++t) {
+      bar_init(sfull(t), 1);
+      bar_init(pfull(t), kRows);
+      bar_init(ofull(t), 1);
+    }
+    bar_init(qfull, 32 * kSoftWarps);
+    bar_init(drained, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s_u32(tmem_slot)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *tmem_slot;
+  Job job;
+  job.b = job_s[0];
+  job.head = (int)(blockIdx.x % p.kv_heads);
+  job.rq = load_request(p, job.b);
+  job.row0 = job_s[1] * kCtaRows;
+  job.n_rows = (int)min((int64_t)kCtaRows, (int64_t)job.rq.n_q * p.group - job.row0);
+  {
+    const int lo = seen_by(p, job.rq, job.row0 / p.group).x;
+    const int hi = seen_by(p, job.rq, (job.row0 + job.n_rows - 1) / p.group).y;
+    job.key0 = lo / kKeys;
+    job.n_keys = max(0, (hi + kKeys - 1) / kKeys - job.key0);
+  }
+  const int tiles = job.n_rows > kRows ? 2 : 1;
+
+  if (warp < kSoftWarps) {
+    // ===================== softmax: one row a thread =====================
+    const int t = warp >> 2, r = tid & (kRows - 1);
+    const int row = t * kRows + r;
+    const bool mine_row = row < job.n_rows;
+    const uint32_t packed = (uint32_t)job.row0 + row, ti = packed / p.group;
+    const int head = job.head * p.group + (int)(packed - ti * p.group);
+    const int64_t tok = job.rq.row0 + (int64_t)ti;
+    const int2 see = mine_row ? seen_by(p, job.rq, (int)ti) : make_int2(0, 0);
+    // The row to FP16, scaled by a power of two, into the swizzled Q tile.
+    float factor;
+    {
+      uint8_t* qs = smem + C::kOffQ + t * C::kOperand + r * 128;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + tok * p.ldq + (int64_t)head * D);
+      uint32_t amax = 0;
+      uint4 raw[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) raw[i] = mine_row ? src[i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) amax = max(amax, max(v[k] & 0x7FFFu, (v[k] >> 16) & 0x7FFFu));
+      }
+      const int e = query_exponent(amax);
+      // A negative scale goes to the query, so that larger scores are larger sums.
+      const float up = p.qk_scale < 0.0f ? -pow2(e) : pow2(e);
+      factor = fabsf(p.qk_scale) * pow2(-e);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(bf16_lo(v[k]) * up, bf16_hi(v[k]) * up);
+        *reinterpret_cast<uint4*>(qs + (i >> 3) * C::kHalfBytes + (((i & 7) ^ (r & 7)) * 16)) =
+            make_uint4(h[0], h[1], h[2], h[3]);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      bar_arrive(qfull);
+    }
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + lanes + C::kTmemS + t * kKeys, to = tmem + lanes + C::kTmemO + t * D;
+    float m = -INFINITY, l = 0.0f;
+    bool ok = true;
+    if (t < tiles) {
+      // Key range that every row of this warp sees, for tiles that need no mask.
+      int lo_max = mine_row ? see.x : 0, hi_min = mine_row ? see.y : 0x7FFFFFFF;
+      lo_max = __reduce_max_sync(0xFFFFFFFFu, lo_max);
+      hi_min = __reduce_min_sync(0xFFFFFFFFu, hi_min);
+      for (int j = 0; j < job.n_keys; ++j) {
+        if (!warp_wait(sfull(t), j & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint64_t live = live_s[j % kLive];
+        const int tok0 = (job.key0 + j) * kKeys;
+        const bool edge = live != 0x0101010101010101ull || tok0 < lo_max || tok0 + kKeys > hi_min;
+        // Row-relative bounds of the keys seen in this tile.
+        const int c_lo = see.x - tok0, c_hi = see.y - tok0;
+        auto seen = [&](int c) { return c >= c_lo && c < c_hi && ((live >> (8 * (c >> 4))) & 1u); };
+        uint32_t v[32];
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kKeys / 32; ++c) {
+          tmem_load_32(ts + 32 * c, v);
+          tmem_wait_32(v);
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) top = fmaxf(top, seen(32 * c + i) ? __uint_as_float(v[i]) : -INFINITY);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+          }
+        }
+        if (top != -INFINITY) top *= factor;
+        if (__any_sync(0xFFFFFFFFu, top > m + kRaise)) {
+          const float mn = fmaxf(m, top);
+          const float keep = m == mn ? 1.0f : exp2_fast(m - mn);
+          m = mn;
+          l *= keep;
+          if (j > 0) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              tmem_load_32(to + 32 * c, v);
+              tmem_wait_32(v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * keep);
+              tmem_store_32(to + 32 * c, v);
+            }
+          }
+        }
+        const float off = m == -INFINITY ? 0.0f : kHead - m;
+#pragma unroll
+        for (int c = 0; c < kKeys / 32; ++c) {
+          tmem_load_32(ts + 32 * c, v);
+          tmem_wait_32(v);
+          uint32_t h[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float a = exp2_fast(fmaf(__uint_as_float(v[2 * i]), factor, off));
+            float b = exp2_fast(fmaf(__uint_as_float(v[2 * i + 1]), factor, off));
+            if (edge) {
+              a = seen(32 * c + 2 * i) ? a : 0.0f;
+              b = seen(32 * c + 2 * i + 1) ? b : 0.0f;
+            }
+            l += a + b;
+            h[i] = pack_f16x2(a, b);
+          }
+          tmem_store_16(ts + 16 * c, h);
+        }
+        tmem_stored();
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        bar_arrive(pfull(t));
+      }
+      if (ok && job.n_keys > 0) ok = warp_wait(ofull(t), 0, abort_flag);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      if (ok) {
+        const float inv = l > 0.0f ? p.v_gscale / l : (l == 0.0f ? 0.0f : l);
+        uint16_t* dst = p.out + tok * p.ldo + (int64_t)head * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          if (job.n_keys > 0) {
+            tmem_load_32(to + 32 * c, v);
+            tmem_wait_32(v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0;
+          }
+          if (mine_row) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * k]) * inv, __uint_as_float(v[8 * i + 2 * k + 1]) * inv);
+              reinterpret_cast<uint4*>(dst)[4 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (mine_row && p.lse != nullptr)
+          p.lse[tok * p.q_heads + head] = l == 0.0f ? -INFINITY : (m - kHead + log2f(l)) * 0.6931471805599453f;
+      }
+    }
+  } else if (warp < kMmaWarp) {
+    // ===================== feeding K and V =====================
+    const int x = tid - 32 * kSoftWarps;
+    constexpr int kCpr = D / 32;                 // 16-byte pieces (32 elements) of a row of codes
+    constexpr int kPieces = kKeys * kCpr / 128;  // per thread and tile: 4 or 2
+    const int part = x % kCpr;
+    const int row_in = x / kCpr;                 // + piece * (128 / kCpr)
+    struct Codes {
+      uint4 k[kPieces], v[kPieces];
+      uint32_t ks[kPieces], vs[kPieces];
+      uint32_t live;
+    } cur, nxt;
+    auto load = [&](int j, Codes& c) {
+      c.live = 0;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int row = row_in + i * (128 / kCpr), tk = (job.key0 + j) * kKeys + row;
+        int page = -1;
+        if ((tk & ~15) < job.rq.hi) page = p.table[(int64_t)job.b * p.max_pages + (tk >> p.page_shift)];
+        const bool live = page >= 0 && page < p.num_pages;
+        c.live |= live ? 1u << i : 0u;
+        c.k[i] = c.v[i] = make_uint4(0, 0, 0, 0);
+        c.ks[i] = c.vs[i] = 0;
+        if (live && tk < job.rq.hi) {  // others: zeros, so that nothing of a page's rest gets into a sum
+          const int64_t at = (((int64_t)page * p.kv_heads + job.head) << p.page_shift) + (tk & ((1 << p.page_shift) - 1));
+          c.k[i] = *reinterpret_cast<const uint4*>(p.k_codes + at * (D / 2) + 16 * part);
+          c.v[i] = *reinterpret_cast<const uint4*>(p.v_codes + at * (D / 2) + 16 * part);
+          c.ks[i] = *reinterpret_cast<const uint16_t*>(p.k_scales + at * (D / 16) + 2 * part);
+          c.vs[i] = *reinterpret_cast<const uint16_t*>(p.v_scales + at * (D / 16) + 2 * part);
+        }
+      }
+    };
+    // 32 elements to four 16-byte pieces of a swizzled row.
+    auto put = [&](uint8_t* base, int row, const uint4& codes, uint32_t scales) {
+      const uint32_t h = e4m3x2_to_f16x2(scales);
+      const uint32_t s0 = __byte_perm(h, h, 0x1010), s1 = __byte_perm(h, h, 0x3232);
+      const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+      uint8_t* dst = base + (D == 128 ? (part >> 1) * C::kHalfBytes : 0) + row * 128;
+      uint4 o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t s = k < 2 ? s0 : s1;
+        o[k] = make_uint4(hmul2(e2m1x2_to_f16x2<0>(w[k]), s), hmul2(e2m1x2_to_f16x2<1>(w[k]), s),
+                          hmul2(e2m1x2_to_f16x2<2>(w[k]), s), hmul2(e2m1x2_to_f16x2<3>(w[k]), s));
+      }
+      const bool turn = D == 128 && (part & 2);  // lanes of the two halves take their pieces in another order: no bank twice
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 val = turn ? o[k ^ 2] : o[k];
+        const int c = (part & 1) * 4 + (turn ? k ^ 2 : k);
+        *reinterpret_cast<uint4*>(dst + ((c ^ (row & 7)) * 16)) = val;
+      }
+    };
+    if (job.n_keys > 0) load(0, cur);
+    for (int j = 0; j < job.n_keys; ++j) {
+      const int s = j % kStages;
+      const uint32_t parity = ((j / kStages) & 1) ^ 1u;
+      if (j + 1 < job.n_keys) load(j + 1, nxt);
+      if (!warp_wait(kempty(s), parity, abort_flag)) break;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int row = row_in + i * (128 / kCpr);
+        put(smem + C::kOffK + s * C::kOperand, row, cur.k[i], cur.ks[i]);
+        if (part == 0 && (row & 15) == 0)
+          reinterpret_cast<uint8_t*>(live_s + j % kLive)[row >> 4] = (cur.live >> i) & 1u;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      bar_arrive(kfull(s));
+      if (!warp_wait(vempty(s), parity, abort_flag)) break;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        put(smem + C::kOffV + s * C::kOperand, row_in + i * (128 / kCpr), cur.v[i], cur.vs[i]);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      bar_arrive(vfull(s));
+      cur = nxt;
+    }
+  } else {
+    // ===================== the products =====================
+    auto scores = [&](int t, int s) {  // S_t = Q_t K^T
+      const uint64_t a = sw128_desc(sbase + C::kOffQ + t * C::kOperand, 16);
+      const uint64_t b = sw128_desc(sbase + C::kOffK + s * C::kOperand, 16);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint64_t step = (uint64_t)(((k >> 2) * C::kHalfBytes + (k & 3) * 32) >> 4);
+        mma_ss(tmem + C::kTmemS + t * kKeys, a + step, b + step, idesc(kKeys, false), k > 0);
+      }
+    };
+    auto output = [&](int t, int s, bool accumulate) {  // O_t += P_t V
+      const uint64_t b = sw128_desc(sbase + C::kOffV + s * C::kOperand, C::kHalfBytes);
+#pragma unroll
+      for (int k = 0; k < kKeys / 16; ++k)
+        mma_ts(tmem + C::kTmemO + t * D, tmem + C::kTmemS + t * kKeys + 8 * k, b + (uint64_t)(k * 2048 >> 4),
+               idesc(D, true), accumulate || k > 0);
+    };
+    bool ok = job.n_keys == 0 || (warp_wait(qfull, 0, abort_flag) && warp_wait(kfull(0), 0, abort_flag));
+    if (ok && job.n_keys > 0) {
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      if (elect()) {
+        for (int t = 0; t < tiles; ++t) {
+          scores(t, 0);
+          commit(sfull(t));
+        }
+        commit(kempty(0));
+      }
+      __syncwarp();
+      for (int j = 0; j < job.n_keys && ok; ++j) {
+        const int s = j % kStages, sn = (j + 1) % kStages;
+        const bool more = j + 1 < job.n_keys;
+        ok = warp_wait(vfull(s), (j / kStages) & 1, abort_flag);
+        for (int t = 0; t < tiles && ok; ++t) {
+          ok = warp_wait(pfull(t), j & 1, abort_flag);
+          if (ok && t == 0 && more) ok = warp_wait(kfull(sn), ((j + 1) / kStages) & 1, abort_flag);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (elect()) {
+            output(t, s, j > 0);
+            if (!more) commit(ofull(t));
+            if (t == tiles - 1) commit(vempty(s));
+            if (more) {
+              scores(t, sn);
+              commit(sfull(t));
+              if (t == tiles - 1) commit(kempty(sn));
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (elect()) commit(drained);
+    __syncwarp();
+    bar_drain(drained, 0);
+  }
+
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+}
+
+template <int D>
+cudaError_t launch_prefill(const AttnParams& p, int64_t grid, cudaStream_t s) {
+  using C = Cfg<D>;
+  static DeviceTable configured;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const int cfg = per_device(configured, dev, [](int) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kv_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    return e == cudaSuccess ? 1 : -(int)e;
+  });
+  if (cfg <= 0) return (cudaError_t)(-cfg);
+  kv_prefill_kernel<D><<<(unsigned)grid, kThreads, C::kSmem, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_attn_tiles(const AttnParams& p, const KvAttnShape& shape, cudaStream_t s) {
+  // As many CTAs as there can be tiles: a request's last tile may be short.
+  const int64_t rows = shape.total_q * p.group, most = rows < shape.batch ? rows : shape.batch;
+  const int64_t grid = (rows / (kRows * kTiles) + most) * shape.kv_heads;
+  return shape.head_dim == 128 ? launch_prefill<128>(p, grid, s) : launch_prefill<64>(p, grid, s);
+}
+
+cudaError_t read_and_clear_kv_error(unsigned int* bits) {
+  unsigned int v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_kv_error, sizeof v);
+  if (e != cudaSuccess) return e;
+  e = cudaMemcpyToSymbol(g_kv_error, &zero, sizeof zero);
+  *bits = v;
+  return e;
+}
+
+}  // namespace fh
