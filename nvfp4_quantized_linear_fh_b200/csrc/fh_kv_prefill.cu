@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       const int e = query_exponent(amax);
       // A negative scale goes to the query, so that larger scores are larger sums.
       const float up = p.qk_scale < 0.0f ? -pow2(e) : pow2(e);
-      factor = fabsf(p.qk_scale) * pow2(-e);
+      // Never 0: a hidden score of -inf stays -inf times it.
+      factor = fmaxf(fabsf(p.qk_scale) * pow2(-e), 1.17549435e-38f);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -387,72 +388,91 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       int lo_max = mine_row ? see.x : 0, hi_min = mine_row ? see.y : 0x7FFFFFFF;
       lo_max = __reduce_max_sync(0xFFFFFFFFu, lo_max);
       hi_min = __reduce_min_sync(0xFFFFFFFFu, hi_min);
+      float2 sum = make_float2(0.0f, 0.0f);
       for (int j = 0; j < job.n_keys; ++j) {
         if (!warp_wait(sfull(t), j & 1, abort_flag)) {
           ok = false;
           break;
         }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        uint32_t va[32], vb[32];
+        tmem_load_32(ts, va);
         const uint64_t live = live_s[j % kLive];
         const int tok0 = (job.key0 + j) * kKeys;
         const bool edge = live != 0x0101010101010101ull || tok0 < lo_max || tok0 + kKeys > hi_min;
-        // Row-relative bounds of the keys seen in this tile.
+        // In a tile at an edge, scores of keys not seen become -inf.
         const int c_lo = see.x - tok0, c_hi = see.y - tok0;
-        auto seen = [&](int c) { return c >= c_lo && c < c_hi && ((live >> (8 * (c >> 4))) & 1u); };
-        uint32_t v[32];
+        auto hide = [&](uint32_t(&v)[32], int c) {
+          const int lo = min(max(c_lo - 32 * c, 0), 32), hi = min(max(c_hi - 32 * c, 0), 32);
+          uint32_t seen = (hi == 32 ? ~0u : (1u << hi) - 1u) & ~(lo == 32 ? ~0u : (1u << lo) - 1u);
+          const uint32_t groups = (uint32_t)(live >> (16 * c));
+          seen &= ((groups & 1u) ? 0xFFFFu : 0u) | ((groups & 0x100u) ? 0xFFFF0000u : 0u);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!((seen >> i) & 1u)) v[i] = 0xFF800000u;
+        };
         float top = -INFINITY;
+        auto highest = [&](uint32_t(&v)[32], int c) {
+          if (edge) hide(v, c);
 #pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c) {
-          tmem_load_32(ts + 32 * c, v);
-          tmem_wait_32(v);
-          if (edge) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, seen(32 * c + i) ? __uint_as_float(v[i]) : -INFINITY);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
-          }
+          for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), top);
+        };
+        // Chunk c + 1 is on its way from TMEM while chunk c is worked on.
+#pragma unroll 1
+        for (int c = 0; c < kKeys / 32; c += 2) {
+          tmem_wait_32(va);
+          tmem_load_32(ts + 32 * (c + 1), vb);
+          highest(va, c);
+          tmem_wait_32(vb);
+          tmem_load_32(ts + 32 * ((c + 2) % (kKeys / 32)), va);  // at the end the first again, for the weights
+          highest(vb, c + 1);
         }
         if (top != -INFINITY) top *= factor;
         if (__any_sync(0xFFFFFFFFu, top > m + kRaise)) {
           const float mn = fmaxf(m, top);
           const float keep = m == mn ? 1.0f : exp2_fast(m - mn);
           m = mn;
-          l *= keep;
+          sum.x *= keep;
+          sum.y *= keep;
           if (j > 0) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
-              tmem_load_32(to + 32 * c, v);
-              tmem_wait_32(v);
+              tmem_load_32(to + 32 * c, vb);
+              tmem_wait_32(vb);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * keep);
-              tmem_store_32(to + 32 * c, v);
+              for (int i = 0; i < 32; ++i) vb[i] = __float_as_uint(__uint_as_float(vb[i]) * keep);
+              tmem_store_32(to + 32 * c, vb);
             }
           }
         }
         const float off = m == -INFINITY ? 0.0f : kHead - m;
-#pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c) {
-          tmem_load_32(ts + 32 * c, v);
-          tmem_wait_32(v);
+        auto weigh = [&](uint32_t(&v)[32], int c) {
+          if (edge) hide(v, c);
           uint32_t h[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            float a = exp2_fast(fmaf(__uint_as_float(v[2 * i]), factor, off));
-            float b = exp2_fast(fmaf(__uint_as_float(v[2 * i + 1]), factor, off));
-            if (edge) {
-              a = seen(32 * c + 2 * i) ? a : 0.0f;
-              b = seen(32 * c + 2 * i + 1) ? b : 0.0f;
-            }
-            l += a + b;
-            h[i] = pack_f16x2(a, b);
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                        make_float2(factor, factor), make_float2(off, off));
+            const float2 w = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+            sum = __fadd2_rn(sum, w);
+            h[i] = pack_f16x2(w.x, w.y);
           }
           tmem_store_16(ts + 16 * c, h);
+        };
+#pragma unroll 1
+        for (int c = 0; c < kKeys / 32; c += 2) {
+          tmem_wait_32(va);
+          tmem_load_32(ts + 32 * (c + 1), vb);
+          weigh(va, c);
+          tmem_wait_32(vb);
+          if (c + 2 < kKeys / 32) tmem_load_32(ts + 32 * (c + 2), va);
+          weigh(vb, c + 1);
         }
         tmem_stored();
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         bar_arrive(pfull(t));
       }
+      l = sum.x + sum.y;
       if (ok && job.n_keys > 0) ok = warp_wait(ofull(t), 0, abort_flag);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       if (ok) {
@@ -490,28 +510,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     constexpr int kPieces = kKeys * kCpr / 128;  // per thread and tile: 4 or 2
     const int part = x % kCpr;
     const int row_in = x / kCpr;                 // + piece * (128 / kCpr)
-    struct Codes {
-      uint4 k[kPieces], v[kPieces];
-      uint32_t ks[kPieces], vs[kPieces];
-      uint32_t live;
-    } cur, nxt;
-    auto load = [&](int j, Codes& c) {
-      c.live = 0;
+    // Pages of a key tile's rows (-1: none, or nothing to read there).
+    int pages[kPieces];
+    auto look_up = [&](int j) {
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        const int row = row_in + i * (128 / kCpr), tk = (job.key0 + j) * kKeys + row;
-        int page = -1;
-        if ((tk & ~15) < job.rq.hi) page = p.table[(int64_t)job.b * p.max_pages + (tk >> p.page_shift)];
-        const bool live = page >= 0 && page < p.num_pages;
-        c.live |= live ? 1u << i : 0u;
-        c.k[i] = c.v[i] = make_uint4(0, 0, 0, 0);
-        c.ks[i] = c.vs[i] = 0;
-        if (live && tk < job.rq.hi) {  // others: zeros, so that nothing of a page's rest gets into a sum
-          const int64_t at = (((int64_t)page * p.kv_heads + job.head) << p.page_shift) + (tk & ((1 << p.page_shift) - 1));
-          c.k[i] = *reinterpret_cast<const uint4*>(p.k_codes + at * (D / 2) + 16 * part);
-          c.v[i] = *reinterpret_cast<const uint4*>(p.v_codes + at * (D / 2) + 16 * part);
-          c.ks[i] = *reinterpret_cast<const uint16_t*>(p.k_scales + at * (D / 16) + 2 * part);
-          c.vs[i] = *reinterpret_cast<const uint16_t*>(p.v_scales + at * (D / 16) + 2 * part);
+        const int tk = (job.key0 + j) * kKeys + row_in + i * (128 / kCpr);
+        pages[i] = -1;
+        if (j < job.n_keys && (tk & ~15) < job.rq.hi) pages[i] = p.table[(int64_t)job.b * p.max_pages + (tk >> p.page_shift)];
+      }
+    };
+    struct Codes {
+      uint4 c[kPieces];
+      uint32_t s[kPieces];
+    } kc, vc;
+    int64_t at[kPieces];  // the rows' places in the cache, -1 where there is nothing: zeros then, so that nothing of a
+                          // page's rest gets into a sum
+    uint32_t live = 0;    // bit i: piece i's page is there
+    auto locate = [&](int j) {
+      live = 0;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int tk = (job.key0 + j) * kKeys + row_in + i * (128 / kCpr);
+        const bool there = pages[i] >= 0 && pages[i] < p.num_pages;
+        live |= there ? 1u << i : 0u;
+        at[i] = there && tk < job.rq.hi
+                    ? (((int64_t)pages[i] * p.kv_heads + job.head) << p.page_shift) + (tk & ((1 << p.page_shift) - 1))
+                    : -1;
+      }
+    };
+    auto load = [&](Codes& c, const uint8_t* codes, const uint8_t* scales) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        c.c[i] = make_uint4(0, 0, 0, 0);
+        c.s[i] = 0;
+        if (at[i] >= 0) {
+          c.c[i] = *reinterpret_cast<const uint4*>(codes + at[i] * (D / 2) + 16 * part);
+          c.s[i] = *reinterpret_cast<const uint16_t*>(scales + at[i] * (D / 16) + 2 * part);
         }
       }
     };
@@ -536,28 +571,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         *reinterpret_cast<uint4*>(dst + ((c ^ (row & 7)) * 16)) = val;
       }
     };
-    if (job.n_keys > 0) load(0, cur);
+    // The next tile's codes are on their way while the current one's are converted,
+    // and the table's entries for the one behind it.
+    look_up(0);
+    locate(0);
+    load(kc, p.k_codes, p.k_scales);
+    load(vc, p.v_codes, p.v_scales);
+    look_up(1);
     for (int j = 0; j < job.n_keys; ++j) {
       const int s = j % kStages;
       const uint32_t parity = ((j / kStages) & 1) ^ 1u;
-      if (j + 1 < job.n_keys) load(j + 1, nxt);
       if (!warp_wait(kempty(s), parity, abort_flag)) break;
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int row = row_in + i * (128 / kCpr);
-        put(smem + C::kOffK + s * C::kOperand, row, cur.k[i], cur.ks[i]);
-        if (part == 0 && (row & 15) == 0)
-          reinterpret_cast<uint8_t*>(live_s + j % kLive)[row >> 4] = (cur.live >> i) & 1u;
+        put(smem + C::kOffK + s * C::kOperand, row, kc.c[i], kc.s[i]);
+        if (part == 0 && (row & 15) == 0) reinterpret_cast<uint8_t*>(live_s + j % kLive)[row >> 4] = (live >> i) & 1u;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       bar_arrive(kfull(s));
+      locate(j + 1);
+      load(kc, p.k_codes, p.k_scales);
+      look_up(j + 2);
       if (!warp_wait(vempty(s), parity, abort_flag)) break;
 #pragma unroll
       for (int i = 0; i < kPieces; ++i)
-        put(smem + C::kOffV + s * C::kOperand, row_in + i * (128 / kCpr), cur.v[i], cur.vs[i]);
+        put(smem + C::kOffV + s * C::kOperand, row_in + i * (128 / kCpr), vc.c[i], vc.s[i]);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       bar_arrive(vfull(s));
-      cur = nxt;
+      load(vc, p.v_codes, p.v_scales);
     }
   } else {
     // ===================== the products =====================
