@@ -47,7 +47,10 @@ constexpr int kStages = 2;     // of K and of V
 constexpr int kSoftWarps = 4 * kTiles;
 constexpr int kFeedWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kFeedWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups: three warps of the last one have no work
+// Registers: launched with 128 a thread (512 threads, the whole file); the
+// eight softmax warps take 176, the others keep 80: 256 * 176 + 256 * 80 = 65536.
+constexpr int kSoftRegs = 176, kOtherRegs = 80;
 constexpr int kLive = 4;       // ring of the key tiles' page masks
 constexpr float kRaise = 8.0f;
 constexpr float kHead = 6.0f;
@@ -61,7 +64,7 @@ struct Cfg {
   static constexpr int kOffK = kOffQ + kTiles * kOperand;
   static constexpr int kOffV = kOffK + kStages * kOperand;
   static constexpr int kOffBar = kOffV + kStages * kOperand;
-  static constexpr int kBars = 4 * kStages + 3 * kTiles + 2;
+  static constexpr int kBars = 4 * kStages + 4 * kTiles + 2;
   static constexpr int kOffLive = kOffBar + 8 * kBars;
   static constexpr int kOffMisc = kOffLive + 8 * kLive;
   // At least half of an SM's shared memory, so that no two CTAs of an SM wait for each other's TMEM.
@@ -208,24 +211,24 @@ __device__ __forceinline__ void tmem_wait_32(uint32_t (&v)[32]) {
                : "memory");
 }
 
-__device__ __forceinline__ void tmem_store_32(uint32_t taddr, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32],"
-      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
-      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(v[0]),
-      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
-      "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
-      "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
-      : "memory");
-}
-
 __device__ __forceinline__ void tmem_store_16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16],"
       " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(v[0]),
       "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
       "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+      : "memory");
+}
+
+// 16 columns, complete on return.
+__device__ __forceinline__ void tmem_load_16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
       : "memory");
 }
 
@@ -250,9 +253,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   auto vfull = [&](int s) { return bar0 + 8u * (2 * kStages + s); };
   auto vempty = [&](int s) { return bar0 + 8u * (3 * kStages + s); };
   auto sfull = [&](int t) { return bar0 + 8u * (4 * kStages + t); };            // scores written
-  auto pfull = [&](int t) { return bar0 + 8u * (4 * kStages + kTiles + t); };   // probabilities written
-  auto ofull = [&](int t) { return bar0 + 8u * (4 * kStages + 2 * kTiles + t); };
-  const uint32_t qfull = bar0 + 8u * (4 * kStages + 3 * kTiles);
+  auto pfull = [&](int t, int half) { return bar0 + 8u * (4 * kStages + kTiles + 2 * t + half); };  // P of 64 keys written
+  auto ofull = [&](int t) { return bar0 + 8u * (4 * kStages + 3 * kTiles + t); };
+  const uint32_t qfull = bar0 + 8u * (4 * kStages + 4 * kTiles);
   const uint32_t drained = qfull + 8u;
   uint64_t* live_s = reinterpret_cast<uint64_t*>(smem + C::kOffLive);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
@@ -307,7 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     }
     for (int t = 0; t < kTiles; ++t) {
       bar_init(sfull(t), 1);
-      bar_init(pfull(t), kRows);
+      bar_init(pfull(t, 0), kRows);
+      bar_init(pfull(t, 1), kRows);
       bar_init(ofull(t), 1);
     }
     bar_init(qfull, 32 * kSoftWarps);
@@ -339,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   const int tiles = job.n_rows > kRows ? 2 : 1;
 
   if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ===================== softmax: one row a thread =====================
     const int t = warp >> 2, r = tid & (kRows - 1);
     const int row = t * kRows + r;
@@ -395,38 +400,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
           break;
         }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        uint32_t va[32], vb[32];
-        tmem_load_32(ts, va);
+        // The row's 128 scores, all at once.
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_load_32(ts + 32 * c, v[c]);
         const uint64_t live = live_s[j % kLive];
         const int tok0 = (job.key0 + j) * kKeys;
         const bool edge = live != 0x0101010101010101ull || tok0 < lo_max || tok0 + kKeys > hi_min;
-        // In a tile at an edge, scores of keys not seen become -inf.
-        const int c_lo = see.x - tok0, c_hi = see.y - tok0;
-        auto hide = [&](uint32_t(&v)[32], int c) {
-          const int lo = min(max(c_lo - 32 * c, 0), 32), hi = min(max(c_hi - 32 * c, 0), 32);
-          uint32_t seen = (hi == 32 ? ~0u : (1u << hi) - 1u) & ~(lo == 32 ? ~0u : (1u << lo) - 1u);
-          const uint32_t groups = (uint32_t)(live >> (16 * c));
-          seen &= ((groups & 1u) ? 0xFFFFu : 0u) | ((groups & 0x100u) ? 0xFFFF0000u : 0u);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!((seen >> i) & 1u)) v[i] = 0xFF800000u;
-        };
-        float top = -INFINITY;
-        auto highest = [&](uint32_t(&v)[32], int c) {
-          if (edge) hide(v, c);
+        for (int c = 0; c < 4; ++c) tmem_wait_32(v[c]);
+        if (edge) {  // scores of keys not seen become -inf
+          const int c_lo = see.x - tok0, c_hi = see.y - tok0;
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), top);
-        };
-        // Chunk c + 1 is on its way from TMEM while chunk c is worked on.
-#pragma unroll 1
-        for (int c = 0; c < kKeys / 32; c += 2) {
-          tmem_wait_32(va);
-          tmem_load_32(ts + 32 * (c + 1), vb);
-          highest(va, c);
-          tmem_wait_32(vb);
-          tmem_load_32(ts + 32 * ((c + 2) % (kKeys / 32)), va);  // at the end the first again, for the weights
-          highest(vb, c + 1);
+          for (int c = 0; c < 4; ++c) {
+            const int lo = min(max(c_lo - 32 * c, 0), 32), hi = min(max(c_hi - 32 * c, 0), 32);
+            uint32_t seen = (hi == 32 ? ~0u : (1u << hi) - 1u) & ~(lo == 32 ? ~0u : (1u << lo) - 1u);
+            const uint32_t groups = (uint32_t)(live >> (16 * c));
+            seen &= ((groups & 1u) ? 0xFFFFu : 0u) | ((groups & 0x100u) ? 0xFFFF0000u : 0u);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((seen >> i) & 1u)) v[c][i] = 0xFF800000u;
+          }
         }
+        float tops[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tops[c] = __uint_as_float(v[c][0]);
+#pragma unroll
+          for (int i = 1; i < 31; i += 2)
+            tops[c] = fmaxf(fmaxf(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])), tops[c]);
+          tops[c] = fmaxf(__uint_as_float(v[c][31]), tops[c]);
+        }
+        float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         if (top != -INFINITY) top *= factor;
         if (__any_sync(0xFFFFFFFFu, top > m + kRaise)) {
           const float mn = fmaxf(m, top);
@@ -436,41 +441,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
           sum.y *= keep;
           if (j > 0) {
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              tmem_load_32(to + 32 * c, vb);
-              tmem_wait_32(vb);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_load_16(to + 16 * c, o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) vb[i] = __float_as_uint(__uint_as_float(vb[i]) * keep);
-              tmem_store_32(to + 32 * c, vb);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+              tmem_store_16(to + 16 * c, o);
             }
           }
         }
         const float off = m == -INFINITY ? 0.0f : kHead - m;
-        auto weigh = [&](uint32_t(&v)[32], int c) {
-          if (edge) hide(v, c);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
           uint32_t h[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])),
                                         make_float2(factor, factor), make_float2(off, off));
             const float2 w = make_float2(exp2_fast(x.x), exp2_fast(x.y));
             sum = __fadd2_rn(sum, w);
             h[i] = pack_f16x2(w.x, w.y);
           }
           tmem_store_16(ts + 16 * c, h);
-        };
-#pragma unroll 1
-        for (int c = 0; c < kKeys / 32; c += 2) {
-          tmem_wait_32(va);
-          tmem_load_32(ts + 32 * (c + 1), vb);
-          weigh(va, c);
-          tmem_wait_32(vb);
-          if (c + 2 < kKeys / 32) tmem_load_32(ts + 32 * (c + 2), va);
-          weigh(vb, c + 1);
+          if (c & 1) {  // 64 keys' P: the product may start on them
+            tmem_stored();
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            bar_arrive(pfull(t, c >> 1));
+          }
         }
-        tmem_stored();
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        bar_arrive(pfull(t));
       }
       l = sum.x + sum.y;
       if (ok && job.n_keys > 0) ok = warp_wait(ofull(t), 0, abort_flag);
@@ -504,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       }
     }
   } else if (warp < kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // ===================== feeding K and V =====================
     const int x = tid - 32 * kSoftWarps;
     constexpr int kCpr = D / 32;                 // 16-byte pieces (32 elements) of a row of codes
@@ -554,21 +553,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     auto put = [&](uint8_t* base, int row, const uint4& codes, uint32_t scales) {
       const uint32_t h = e4m3x2_to_f16x2(scales);
       const uint32_t s0 = __byte_perm(h, h, 0x1010), s1 = __byte_perm(h, h, 0x3232);
-      const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+      // Lanes of the row's two halves take their pieces in different orders, so that no bank is asked twice.
+      const bool turn = D == 128 && (part & 2);
+      const uint32_t w[4] = {turn ? codes.z : codes.x, turn ? codes.w : codes.y, turn ? codes.x : codes.z,
+                             turn ? codes.y : codes.w};
+      const uint32_t sa = turn ? s1 : s0, sb = turn ? s0 : s1;
       uint8_t* dst = base + (D == 128 ? (part >> 1) * C::kHalfBytes : 0) + row * 128;
-      uint4 o[4];
+      const int c0 = (part & 1) * 4 + (turn ? 2 : 0);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t s = k < 2 ? s0 : s1;
-        o[k] = make_uint4(hmul2(e2m1x2_to_f16x2<0>(w[k]), s), hmul2(e2m1x2_to_f16x2<1>(w[k]), s),
-                          hmul2(e2m1x2_to_f16x2<2>(w[k]), s), hmul2(e2m1x2_to_f16x2<3>(w[k]), s));
-      }
-      const bool turn = D == 128 && (part & 2);  // lanes of the two halves take their pieces in another order: no bank twice
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint4 val = turn ? o[k ^ 2] : o[k];
-        const int c = (part & 1) * 4 + (turn ? k ^ 2 : k);
-        *reinterpret_cast<uint4*>(dst + ((c ^ (row & 7)) * 16)) = val;
+        const uint32_t s = k < 2 ? sa : sb;
+        *reinterpret_cast<uint4*>(dst + (((c0 ^ k) ^ (row & 7)) * 16)) =
+            make_uint4(hmul2(e2m1x2_to_f16x2<0>(w[k]), s), hmul2(e2m1x2_to_f16x2<1>(w[k]), s),
+                       hmul2(e2m1x2_to_f16x2<2>(w[k]), s), hmul2(e2m1x2_to_f16x2<3>(w[k]), s));
       }
     };
     // The next tile's codes are on their way while the current one's are converted,
@@ -602,6 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       load(vc, p.v_codes, p.v_scales);
     }
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kMmaWarp) {
     // ===================== the products =====================
     auto scores = [&](int t, int s) {  // S_t = Q_t K^T
       const uint64_t a = sw128_desc(sbase + C::kOffQ + t * C::kOperand, 16);
@@ -612,10 +611,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         mma_ss(tmem + C::kTmemS + t * kKeys, a + step, b + step, idesc(kKeys, false), k > 0);
       }
     };
-    auto output = [&](int t, int s, bool accumulate) {  // O_t += P_t V
+    auto output = [&](int t, int s, int half, bool accumulate) {  // O_t += P_t V over 64 keys
       const uint64_t b = sw128_desc(sbase + C::kOffV + s * C::kOperand, C::kHalfBytes);
 #pragma unroll
-      for (int k = 0; k < kKeys / 16; ++k)
+      for (int k = 4 * half; k < 4 * half + 4; ++k)
         mma_ts(tmem + C::kTmemO + t * D, tmem + C::kTmemS + t * kKeys + 8 * k, b + (uint64_t)(k * 2048 >> 4),
                idesc(D, true), accumulate || k > 0);
     };
@@ -635,12 +634,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         const bool more = j + 1 < job.n_keys;
         ok = warp_wait(vfull(s), (j / kStages) & 1, abort_flag);
         for (int t = 0; t < tiles && ok; ++t) {
-          ok = warp_wait(pfull(t), j & 1, abort_flag);
+          ok = warp_wait(pfull(t, 0), j & 1, abort_flag);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (elect()) output(t, s, 0, j > 0);
+          __syncwarp();
+          ok = warp_wait(pfull(t, 1), j & 1, abort_flag);
           if (ok && t == 0 && more) ok = warp_wait(kfull(sn), ((j + 1) / kStages) & 1, abort_flag);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (elect()) {
-            output(t, s, j > 0);
+            output(t, s, 1, true);
             if (!more) commit(ofull(t));
             if (t == tiles - 1) commit(vempty(s));
             if (more) {
@@ -656,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     if (elect()) commit(drained);
     __syncwarp();
     bar_drain(drained, 0);
+    }
   }
 
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
