@@ -10,13 +10,18 @@
 //   warps 0..3, 4..7   one row a thread, a tile each: scores from TMEM, running
 //                      maximum and sum, P back to TMEM over the scores' columns,
 //                      where the second product takes it as its A operand.
-//   warps 8..11        codes from global memory, converted to code * scale in
+//   warps 8..11        codes from shared memory, converted to code * scale in
 //                      FP16 (exact) and laid out in 128-byte swizzled rows; the
 //                      same layout serves K as a K-major operand and V as an
-//                      MN-major one, so V is not transposed.  The next tile's
-//                      codes are in registers while the current one is stored.
+//                      MN-major one, so V is not transposed.
 //   warp 12            issues the products: S = Q K^T of one tile while the other
 //                      tile's softmax runs, O += P V.
+//   warp 13            brings the pages' codes and scales to shared memory with
+//                      cp.async.bulk, three half steps ahead.  (Loads by the
+//                      converting threads would be waited for by the proxy fence
+//                      that hands their stores to the tensor cores: 265 us at
+//                      21 x 4096 x 4096 x 128, where softmax and products alone
+//                      take 232.)
 // The output stays in TMEM.  It is rescaled only when a row's maximum grows by
 // more than 8 (in log2), by the row's own thread: the commit that announces
 // S(j) also covers O += P(j-1) V, so nothing else is writing O then.
@@ -46,8 +51,9 @@ constexpr int kKeys = 128;     // tokens of a key tile
 constexpr int kStages = 2;     // of K and of V
 constexpr int kSoftWarps = 4 * kTiles;
 constexpr int kFeedWarps = 4;
-constexpr int kMmaWarp = kSoftWarps + kFeedWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups: three warps of the last one have no work
+constexpr int kMmaWarp = kSoftWarps + kFeedWarps, kCopyWarp = kMmaWarp + 1;
+constexpr int kRaw = 3;        // ring of tiles' codes and scales, K and V in turns
+constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups: two warps of the last one have no work
 // Registers: launched with 128 a thread (512 threads, the whole file); the
 // eight softmax warps take 176, the others keep 80: 256 * 176 + 256 * 80 = 65536.
 constexpr int kSoftRegs = 176, kOtherRegs = 80;
@@ -63,10 +69,14 @@ struct Cfg {
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + kTiles * kOperand;
   static constexpr int kOffV = kOffK + kStages * kOperand;
-  static constexpr int kOffBar = kOffV + kStages * kOperand;
-  static constexpr int kBars = 4 * kStages + 4 * kTiles + 2;
+  static constexpr int kRawCodes = kKeys * D / 2, kRawScales = kKeys * D / 16;
+  static constexpr int kRawBytes = kRawCodes + kRawScales;
+  static constexpr int kOffRaw = kOffV + kStages * kOperand;
+  static constexpr int kOffBar = kOffRaw + kRaw * kRawBytes;
+  static constexpr int kBars = 4 * kStages + 4 * kTiles + 2 + 2 * kRaw;
   static constexpr int kOffLive = kOffBar + 8 * kBars;
-  static constexpr int kOffMisc = kOffLive + 8 * kLive;
+  static constexpr int kOffRawLive = kOffLive + 8 * kLive;
+  static constexpr int kOffMisc = kOffRawLive + 8 * kRaw;
   // At least half of an SM's shared memory, so that no two CTAs of an SM wait for each other's TMEM.
   static constexpr int kNeed = kOffMisc + 64 + 1024;
   static constexpr int kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
@@ -257,7 +267,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   auto ofull = [&](int t) { return bar0 + 8u * (4 * kStages + 3 * kTiles + t); };
   const uint32_t qfull = bar0 + 8u * (4 * kStages + 4 * kTiles);
   const uint32_t drained = qfull + 8u;
-  uint64_t* live_s = reinterpret_cast<uint64_t*>(smem + C::kOffLive);
+  auto rfull = [&](int i) { return drained + 8u + 8u * i; };
+  auto rempty = [&](int i) { return drained + 8u + 8u * (kRaw + i); };
+  uint64_t* live_s = reinterpret_cast<uint64_t*>(smem + C::kOffLive);     // a byte per 16 keys: their page is there
+  uint64_t* raw_live = reinterpret_cast<uint64_t*>(smem + C::kOffRawLive);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
   int* job_s = reinterpret_cast<int*>(smem + C::kOffMisc + 16);  // request, tile
@@ -316,6 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     }
     bar_init(qfull, 32 * kSoftWarps);
     bar_init(drained, 1);
+    for (int i = 0; i < kRaw; ++i) {
+      bar_init(rfull(i), 1);
+      bar_init(rempty(i), kFeedWarps);
+    }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -509,46 +526,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     constexpr int kPieces = kKeys * kCpr / 128;  // per thread and tile: 4 or 2
     const int part = x % kCpr;
     const int row_in = x / kCpr;                 // + piece * (128 / kCpr)
-    // Pages of a key tile's rows (-1: none, or nothing to read there).
-    int pages[kPieces];
-    auto look_up = [&](int j) {
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int tk = (job.key0 + j) * kKeys + row_in + i * (128 / kCpr);
-        pages[i] = -1;
-        if (j < job.n_keys && (tk & ~15) < job.rq.hi) pages[i] = p.table[(int64_t)job.b * p.max_pages + (tk >> p.page_shift)];
-      }
-    };
-    struct Codes {
-      uint4 c[kPieces];
-      uint32_t s[kPieces];
-    } kc, vc;
-    int64_t at[kPieces];  // the rows' places in the cache, -1 where there is nothing: zeros then, so that nothing of a
-                          // page's rest gets into a sum
-    uint32_t live = 0;    // bit i: piece i's page is there
-    auto locate = [&](int j) {
-      live = 0;
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int tk = (job.key0 + j) * kKeys + row_in + i * (128 / kCpr);
-        const bool there = pages[i] >= 0 && pages[i] < p.num_pages;
-        live |= there ? 1u << i : 0u;
-        at[i] = there && tk < job.rq.hi
-                    ? (((int64_t)pages[i] * p.kv_heads + job.head) << p.page_shift) + (tk & ((1 << p.page_shift) - 1))
-                    : -1;
-      }
-    };
-    auto load = [&](Codes& c, const uint8_t* codes, const uint8_t* scales) {
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        c.c[i] = make_uint4(0, 0, 0, 0);
-        c.s[i] = 0;
-        if (at[i] >= 0) {
-          c.c[i] = *reinterpret_cast<const uint4*>(codes + at[i] * (D / 2) + 16 * part);
-          c.s[i] = *reinterpret_cast<const uint16_t*>(scales + at[i] * (D / 16) + 2 * part);
-        }
-      }
-    };
     // 32 elements to four 16-byte pieces of a swizzled row.
     auto put = [&](uint8_t* base, int row, const uint4& codes, uint32_t scales) {
       const uint32_t h = e4m3x2_to_f16x2(scales);
@@ -568,35 +545,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
                        hmul2(e2m1x2_to_f16x2<2>(w[k]), s), hmul2(e2m1x2_to_f16x2<3>(w[k]), s));
       }
     };
-    // The next tile's codes are on their way while the current one's are converted,
-    // and the table's entries for the one behind it.
-    look_up(0);
-    locate(0);
-    load(kc, p.k_codes, p.k_scales);
-    load(vc, p.v_codes, p.v_scales);
-    look_up(1);
-    for (int j = 0; j < job.n_keys; ++j) {
-      const int s = j % kStages;
-      const uint32_t parity = ((j / kStages) & 1) ^ 1u;
-      if (!warp_wait(kempty(s), parity, abort_flag)) break;
+    bool ok = true;
+    for (int n = 0; n < 2 * job.n_keys && ok; ++n) {  // K and V of a tile in turns
+      const int j = n >> 1, s = j % kStages, slot = n % kRaw;
+      const bool is_v = n & 1;
+      ok = warp_wait(rfull(slot), (n / kRaw) & 1, abort_flag);
+      if (!ok) break;
+      const uint8_t* raw = smem + C::kOffRaw + slot * C::kRawBytes;
+      const uint64_t live = raw_live[slot];
+      uint4 codes[kPieces];
+      uint32_t scales[kPieces];
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int row = row_in + i * (128 / kCpr);
-        put(smem + C::kOffK + s * C::kOperand, row, kc.c[i], kc.s[i]);
-        if (part == 0 && (row & 15) == 0) reinterpret_cast<uint8_t*>(live_s + j % kLive)[row >> 4] = (live >> i) & 1u;
+        codes[i] = *reinterpret_cast<const uint4*>(raw + row * (D / 2) + 16 * part);
+        scales[i] = *reinterpret_cast<const uint16_t*>(raw + C::kRawCodes + row * (D / 16) + 2 * part);
+        // Rows of no token get scales of 0, so that nothing of a page's rest gets into a sum.
+        if (!((live >> (8 * (row >> 4))) & 1u) || (job.key0 + j) * kKeys + row >= job.rq.hi) scales[i] = 0;
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      bar_arrive(kfull(s));
-      locate(j + 1);
-      load(kc, p.k_codes, p.k_scales);
-      look_up(j + 2);
-      if (!warp_wait(vempty(s), parity, abort_flag)) break;
+      __syncwarp();
+      if (lane == 0) bar_arrive(rempty(slot));
+      ok = warp_wait(is_v ? vempty(s) : kempty(s), ((j / kStages) & 1) ^ 1u, abort_flag);
+      if (!ok) break;
+      uint8_t* dst = smem + (is_v ? C::kOffV : C::kOffK) + s * C::kOperand;
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i)
-        put(smem + C::kOffV + s * C::kOperand, row_in + i * (128 / kCpr), vc.c[i], vc.s[i]);
+      for (int i = 0; i < kPieces; ++i) put(dst, row_in + i * (128 / kCpr), codes[i], scales[i]);
+      if (!is_v && x == 0) live_s[j % kLive] = live;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      bar_arrive(vfull(s));
-      load(vc, p.v_codes, p.v_scales);
+      bar_arrive(is_v ? vfull(s) : kfull(s));
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -660,6 +636,58 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     if (elect()) commit(drained);
     __syncwarp();
     bar_drain(drained, 0);
+    } else if (warp == kCopyWarp) {
+      // ===================== bringing codes and scales =====================
+      // Lanes 0..7: codes of a tile's (up to eight) pieces of a page each, lanes
+      // 8..15: their scales.  Sizes are multiples of 16 tokens, so of 16 bytes.
+      const int shift = min(p.page_shift, 7), piece = lane & 7;  // 2^shift tokens a piece
+      const bool is_scale = lane & 8;
+      const uint32_t per_token = is_scale ? D / 16 : D / 2;
+      const bool mine_piece = lane < 16 && piece < (kKeys >> shift);
+      auto look_up = [&](int j) {  // the piece's page, -1 where there is none or nothing to read
+        const int tk = (job.key0 + j) * kKeys + (piece << shift);
+        if (!mine_piece || j >= job.n_keys || tk >= job.rq.hi) return -1;
+        const int page = p.table[(int64_t)job.b * p.max_pages + (tk >> p.page_shift)];
+        return page < p.num_pages ? page : -1;
+      };
+      int page = look_up(0);
+      int issued = 0;
+      for (int j = 0; j < job.n_keys; ++j) {
+        const int next = look_up(j + 1);
+        const int tk = (job.key0 + j) * kKeys + (piece << shift);
+        const int tokens = page >= 0 ? min(1 << shift, (job.rq.hi - tk + 15) & ~15) : 0;
+        const int64_t at = page >= 0 ? (((int64_t)page * p.kv_heads + job.head) << p.page_shift) + (tk & ((1 << p.page_shift) - 1)) : 0;
+        const uint32_t bytes = tokens * per_token;
+        const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, bytes);
+        // Group g of 16 tokens lies in piece g >> (shift - 4).
+        const int g_tokens = __shfl_sync(0xFFFFFFFFu, tokens, piece >> (shift - 4));
+        const bool g_live = g_tokens > 16 * (piece & ((1 << (shift - 4)) - 1));
+        bool ok = true;
+        for (int v = 0; v < 2 && ok; ++v) {
+          const int n = 2 * j + v, slot = n % kRaw;
+          ok = warp_wait(rempty(slot), ((n / kRaw) & 1) ^ 1u, abort_flag);
+          if (!ok) break;
+          if (lane < 8) reinterpret_cast<uint8_t*>(raw_live + slot)[lane] = g_live ? 1 : 0;
+          __syncwarp();
+          if (lane == 0)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(rfull(slot)), "r"(total) : "memory");
+          __syncwarp();
+          if (bytes != 0) {
+            const uint8_t* src = (is_scale ? (v ? p.v_scales : p.k_scales) : (v ? p.v_codes : p.k_codes)) + at * per_token;
+            const uint32_t dst = sbase + C::kOffRaw + slot * C::kRawBytes + (is_scale ? C::kRawCodes : 0) +
+                                 (uint32_t)(piece << shift) * per_token;
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                "l"(src), "r"(bytes), "r"(rfull(slot))
+                : "memory");
+          }
+          ++issued;
+        }
+        if (!ok) break;
+        page = next;
+      }
+      // Copies in flight end before the CTA does.
+      for (int n = max(0, issued - kRaw); n < issued; ++n) bar_drain(rfull(n % kRaw), (n / kRaw) & 1);
     }
   }
 
