@@ -95,6 +95,12 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// One arrival for the warp (128 threads arriving one by one queue up on the barrier's word).
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+  __syncwarp();
+  if (lane == 0) bar_arrive(bar);
+}
+
 __device__ __forceinline__ bool bar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -316,18 +322,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   }
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      bar_init(kfull(s), 32 * kFeedWarps);
+      bar_init(kfull(s), kFeedWarps);
       bar_init(kempty(s), 1);
-      bar_init(vfull(s), 32 * kFeedWarps);
+      bar_init(vfull(s), kFeedWarps);
       bar_init(vempty(s), 1);
     }
     for (int t = 0; t < kTiles; ++t) {
       bar_init(sfull(t), 1);
-      bar_init(pfull(t, 0), kRows);
-      bar_init(pfull(t, 1), kRows);
+      bar_init(pfull(t, 0), 4);
+      bar_init(pfull(t, 1), 4);
       bar_init(ofull(t), 1);
     }
-    bar_init(qfull, 32 * kSoftWarps);
+    bar_init(qfull, kSoftWarps);
     bar_init(drained, 1);
     for (int i = 0; i < kRaw; ++i) {
       bar_init(rfull(i), 1);
@@ -399,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
             make_uint4(h[0], h[1], h[2], h[3]);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      bar_arrive(qfull);
+      warp_arrive(qfull, lane);
     }
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + C::kTmemS + t * kKeys, to = tmem + lanes + C::kTmemO + t * D;
@@ -483,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
           if (c & 1) {  // 64 keys' P: the product may start on them
             tmem_stored();
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            bar_arrive(pfull(t, c >> 1));
+            warp_arrive(pfull(t, c >> 1), lane);
           }
         }
       }
@@ -563,8 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         // Rows of no token get scales of 0, so that nothing of a page's rest gets into a sum.
         if (!((live >> (8 * (row >> 4))) & 1u) || (job.key0 + j) * kKeys + row >= job.rq.hi) scales[i] = 0;
       }
-      __syncwarp();
-      if (lane == 0) bar_arrive(rempty(slot));
+      warp_arrive(rempty(slot), lane);
       ok = warp_wait(is_v ? vempty(s) : kempty(s), ((j / kStages) & 1) ^ 1u, abort_flag);
       if (!ok) break;
       uint8_t* dst = smem + (is_v ? C::kOffV : C::kOffK) + s * C::kOperand;
@@ -572,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       for (int i = 0; i < kPieces; ++i) put(dst, row_in + i * (128 / kCpr), codes[i], scales[i]);
       if (!is_v && x == 0) live_s[j % kLive] = live;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      bar_arrive(is_v ? vfull(s) : kfull(s));
+      warp_arrive(is_v ? vfull(s) : kfull(s), lane);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
