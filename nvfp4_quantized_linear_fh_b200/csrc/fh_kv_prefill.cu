@@ -375,34 +375,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     const int head = job.head * p.group + (int)(packed - ti * p.group);
     const int64_t tok = job.rq.row0 + (int64_t)ti;
     const int2 see = mine_row ? seen_by(p, job.rq, (int)ti) : make_int2(0, 0);
-    // The row to FP16, scaled by a power of two, into the swizzled Q tile.
-    float factor;
+    // The warp's 32 rows to FP16, each scaled by a power of two, into the swizzled
+    // Q tile.  kPer lanes take a row together, so that a load covers whole lines
+    // (a row a lane takes 32 lines a load: 4500 cycles a CTA, and as many to store).
+    constexpr int kPer = D / 8, kPerLoad = 32 / kPer;  // lanes of a row, rows of a load
+    const int64_t q_at = tok * p.ldq + (int64_t)head * D, o_at = tok * p.ldo + (int64_t)head * D;
+    const int piece = lane % kPer;
+    float factor = 0.0f;
     {
-      uint8_t* qs = smem + C::kOffQ + t * C::kOperand + r * 128;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + tok * p.ldq + (int64_t)head * D);
-      uint32_t amax = 0;
-      uint4 raw[D / 8];
+      uint4 raw[kPer];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) raw[i] = mine_row ? src[i] : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < kPer; ++i) {
+        const int src = i * kPerLoad + lane / kPer;
+        const int64_t at = __shfl_sync(0xFFFFFFFFu, q_at, src);
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (t * kRows + 32 * (warp & 3) + src < job.n_rows) raw[i] = *reinterpret_cast<const uint4*>(p.q + at + 8 * piece);
+      }
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
+      for (int i = 0; i < kPer; ++i) {
         const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t amax = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) amax = max(amax, max(v[k] & 0x7FFFu, (v[k] >> 16) & 0x7FFFu));
-      }
-      const int e = query_exponent(amax);
-      // A negative scale goes to the query, so that larger scores are larger sums.
-      const float up = p.qk_scale < 0.0f ? -pow2(e) : pow2(e);
-      // Never 0: a hidden score of -inf stays -inf times it.
-      factor = fmaxf(fabsf(p.qk_scale) * pow2(-e), 1.17549435e-38f);
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        for (int o = 1; o < kPer; o <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        const int e = query_exponent(amax);
+        // A negative scale goes to the query, so that larger scores are larger sums.
+        const float up = p.qk_scale < 0.0f ? -pow2(e) : pow2(e);
         uint32_t h[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(bf16_lo(v[k]) * up, bf16_hi(v[k]) * up);
-        *reinterpret_cast<uint4*>(qs + (i >> 3) * C::kHalfBytes + (((i & 7) ^ (r & 7)) * 16)) =
-            make_uint4(h[0], h[1], h[2], h[3]);
+        const int qr = 32 * (warp & 3) + i * kPerLoad + lane / kPer;
+        *reinterpret_cast<uint4*>(smem + C::kOffQ + t * C::kOperand + (piece >> 3) * C::kHalfBytes + qr * 128 +
+                                  (((piece & 7) ^ (qr & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
+        // Never 0: a hidden score of -inf stays -inf times it.
+        const float f = fmaxf(fabsf(p.qk_scale) * pow2(-e), 1.17549435e-38f);
+        const float mine = __shfl_sync(0xFFFFFFFFu, f, (lane % kPerLoad) * kPer);
+        if (lane / kPerLoad == i) factor = mine;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       warp_arrive(qfull, lane);
@@ -498,7 +507,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       if (ok) {
         const float inv = l > 0.0f ? p.v_gscale / l : (l == 0.0f ? 0.0f : l);
-        uint16_t* dst = p.out + tok * p.ldo + (int64_t)head * D;
+        // Through shared memory (this warp's part of its Q tile, which the products
+        // are done with), so that the stores cover whole lines.
+        uint8_t* stage = smem + C::kOffQ + t * C::kOperand + (warp & 3) * (32 * D * 2);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
@@ -509,16 +520,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0;
           }
-          if (mine_row) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w[4];
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * k]) * inv, __uint_as_float(v[8 * i + 2 * k + 1]) * inv);
-              reinterpret_cast<uint4*>(dst)[4 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * k]) * inv, __uint_as_float(v[8 * i + 2 * k + 1]) * inv);
+            *reinterpret_cast<uint4*>(stage + lane * (2 * D) + (((4 * c + i) ^ (lane & 7)) * 16)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int src = i * kPerLoad + lane / kPer;
+          const int64_t at = __shfl_sync(0xFFFFFFFFu, o_at, src);
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + src * (2 * D) + ((piece ^ (src & 7)) * 16));
+          if (t * kRows + 32 * (warp & 3) + src < job.n_rows) *reinterpret_cast<uint4*>(p.out + at + 8 * piece) = w;
         }
         if (mine_row && p.lse != nullptr)
           p.lse[tok * p.q_heads + head] = l == 0.0f ? -INFINITY : (m - kHead + log2f(l)) * 0.6931471805599453f;
@@ -599,46 +617,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
         mma_ts(tmem + C::kTmemO + t * D, tmem + C::kTmemS + t * kKeys + 8 * k, b + (uint64_t)(k * 2048 >> 4),
                idesc(D, true), accumulate || k > 0);
     };
-    bool ok = job.n_keys == 0 || (warp_wait(qfull, 0, abort_flag) && warp_wait(kfull(0), 0, abort_flag));
-    if (ok && job.n_keys > 0) {
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      if (elect()) {
+    if (elect()) {  // one thread waits and issues: no votes between a wait and its product
+      bool ok = job.n_keys > 0 && bar_wait(qfull, 0, abort_flag) && bar_wait(kfull(0), 0, abort_flag);
+      if (ok) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         for (int t = 0; t < tiles; ++t) {
           scores(t, 0);
           commit(sfull(t));
         }
         commit(kempty(0));
       }
-      __syncwarp();
       for (int j = 0; j < job.n_keys && ok; ++j) {
         const int s = j % kStages, sn = (j + 1) % kStages;
         const bool more = j + 1 < job.n_keys;
-        ok = warp_wait(vfull(s), (j / kStages) & 1, abort_flag);
+        ok = bar_wait(vfull(s), (j / kStages) & 1, abort_flag) &&
+             (!more || bar_wait(kfull(sn), ((j + 1) / kStages) & 1, abort_flag));
         for (int t = 0; t < tiles && ok; ++t) {
-          ok = warp_wait(pfull(t, 0), j & 1, abort_flag);
+          ok = bar_wait(pfull(t, 0), j & 1, abort_flag);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          if (elect()) output(t, s, 0, j > 0);
-          __syncwarp();
-          ok = warp_wait(pfull(t, 1), j & 1, abort_flag);
-          if (ok && t == 0 && more) ok = warp_wait(kfull(sn), ((j + 1) / kStages) & 1, abort_flag);
+          output(t, s, 0, j > 0);
+          ok = bar_wait(pfull(t, 1), j & 1, abort_flag);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          if (elect()) {
-            output(t, s, 1, true);
-            if (!more) commit(ofull(t));
-            if (t == tiles - 1) commit(vempty(s));
-            if (more) {
-              scores(t, sn);
-              commit(sfull(t));
-              if (t == tiles - 1) commit(kempty(sn));
-            }
+          output(t, s, 1, true);
+          if (!more) commit(ofull(t));
+          if (more) {
+            scores(t, sn);
+            commit(sfull(t));
           }
-          __syncwarp();
+          if (t == tiles - 1) {
+            commit(vempty(s));
+            if (more) commit(kempty(sn));
+          }
         }
       }
+      commit(drained);
     }
-    if (elect()) commit(drained);
     __syncwarp();
     bar_drain(drained, 0);
     } else if (warp == kCopyWarp) {
