@@ -122,13 +122,16 @@ __device__ __forceinline__ uint64_t now_ns() {
 // Bounded wait (~4 s, or until another role gave up): sets the error word and
 // the CTA's abort flag on expiry.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (bar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = now_ns();
+  uint64_t t0 = 0;
   for (uint32_t i = 1; i < (1u << 30); ++i) {
     if (bar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0u) {
+    // The clock is looked at late and seldom: reading it takes about 900
+    // cycles, in which the barrier is not seen to complete.
+    if ((i & 1023u) == 0u) {
       if (*abort) return false;
-      if (now_ns() - t0 > 4000000000ull) break;
+      const uint64_t now = now_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > 4000000000ull) break;
     }
   }
   atomicOr(&g_kv_error, (unsigned)kDevErrTimeout);
