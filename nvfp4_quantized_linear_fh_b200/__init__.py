@@ -466,7 +466,7 @@ class KVCache:
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = shape
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.k_gscale, self.v_gscale = float(k_gscale), float(v_gscale)
-        self.device = k_codes.device
+        self.device, self.index = k_codes.device, k_codes.get_device()
         self._c = _CKVCache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
                             self.num_pages, self.page_size, self.kv_heads, self.head_dim, self.k_gscale,
                             self.v_gscale)
@@ -481,22 +481,30 @@ def empty_kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int,
     return KVCache(new(2), new(16), new(2), new(16), k_gscale, v_gscale)
 
 
-def _need_all(device, dtype, **tensors):
-    """Contiguous tensors of one dtype on `device`, which is the current one: the library launches there."""
-    for n, t in tensors.items():
-        if not isinstance(t, torch.Tensor) or t.dtype != dtype:
-            raise TypeError(f"{n} must be a tensor of {dtype}")
-        if t.device != device:
-            raise ValueError(f"{n} must be on {device}")
+# The cache's calls run once a layer and token, some for a few microseconds: their checks are written for few
+# attribute reads (a device is compared by its index, the stream is read as the raw handle).
+
+def _need_all(index, dtype, names, *tensors):
+    """Contiguous tensors of one dtype on CUDA device `index`."""
+    for t in tensors:
+        if type(t) is not torch.Tensor and not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+            raise TypeError(f"{names} must be tensors of {dtype}")
+        if t.get_device() != index:
+            raise ValueError(f"{names} must be on cuda:{index}")
         if not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
+            raise ValueError(f"{names} must be contiguous")
 
 
-def _need_current(device):
-    if device.type != "cuda":
+def _need_current(index):
+    """The library launches on the current device."""
+    if index < 0:
         raise TypeError("tensors must be CUDA tensors")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, which is not the current device")
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors are on cuda:{index}, which is not the current device")
+
+
+def _raw_stream(stream, index):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def fh_kv_pages_update(held: torch.Tensor, target: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -509,11 +517,11 @@ def fh_kv_pages_update(held: torch.Tensor, target: torch.Tensor, block_table: to
     target, free_count_out may be free_count."""
     if not isinstance(held, torch.Tensor):
         raise TypeError("held must be a tensor")
-    device = held.device
-    _need_current(device)
-    _need_all(device, torch.int32, held=held, target=target, block_table=block_table, free_pages=free_pages,
-              free_count=free_count, free_count_out=free_count_out, lens=lens, q_starts=q_starts, status=status)
-    _need_all(device, torch.int64, slots=slots)
+    index = held.get_device()
+    _need_current(index)
+    _need_all(index, torch.int32, "held, target, block_table, free_pages, free_count, free_count_out, lens, q_starts, "
+              "status", held, target, block_table, free_pages, free_count, free_count_out, lens, q_starts, status)
+    _need_all(index, torch.int64, "slots", slots)
     n = held.numel()
     if (target.numel() != n or lens.numel() != n or q_starts.numel() != n + 1 or block_table.dim() != 2
             or block_table.shape[0] != n or free_count.numel() != 1 or free_count_out.numel() != 1
@@ -524,14 +532,15 @@ def fh_kv_pages_update(held: torch.Tensor, target: torch.Tensor, block_table: to
                                    block_table.shape[1], free_pages.data_ptr(), free_pages.numel(),
                                    free_count.data_ptr(), free_count_out.data_ptr(), lens.data_ptr(),
                                    q_starts.data_ptr(), slots.data_ptr(), slots.numel(), status.data_ptr(),
-                                   _stream(stream)))
+                                   _raw_stream(stream, index)))
 
 
 def _kv_rows(cache, t, tokens, what):
     """The token stride of BF16 rows [tokens, kv_heads, head_dim] of the cache's heads."""
-    _need(t, _BF16, what, 3)
-    if t.device != cache.device:
-        raise ValueError(f"{what} must be on {cache.device}")
+    if not isinstance(t, torch.Tensor) or t.dtype not in _BF16:
+        raise TypeError(f"{what} must be a BF16 tensor")
+    if t.get_device() != cache.index:
+        raise ValueError(f"{what} must be on cuda:{cache.index}")
     if t.shape != (tokens, cache.kv_heads, cache.head_dim):
         raise ValueError(f"{what} must have the shape [tokens, kv_heads, head_dim] of slots and cache")
     return _row_stride(t, what)
@@ -541,7 +550,7 @@ def _row_stride(t, what):
     """The token stride of [tokens, heads, d] rows, whose heads must lie one after the other."""
     tokens, heads, d = t.shape
     s = t.stride()
-    if (s[2] != 1 and d > 1) or (s[1] != d and heads > 1):
+    if s[2] != 1 or (s[1] != d and heads > 1):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
     return s[0] if tokens > 1 else heads * d
 
@@ -550,27 +559,29 @@ def fh_kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: t
                       clip_count: torch.Tensor | None = None, stream=None) -> None:
     """Quantize BF16 k, v [tokens, kv_heads, head_dim] (any token stride) into the cache's slots (int64 [tokens];
     negative: left out; distinct); clip_count (int64, 1 element) += elements beyond the scales' range."""
-    _need_current(cache.device)
-    _need_all(cache.device, torch.int64, slots=slots)
+    index = cache.index
+    _need_current(index)
+    _need_all(index, torch.int64, "slots", slots)
     n = slots.numel()
     ldk, ldv = _kv_rows(cache, k, n, "k"), _kv_rows(cache, v, n, "v")
     if clip_count is not None:
-        _need_all(cache.device, torch.int64, clip_count=clip_count)
+        _need_all(index, torch.int64, "clip_count", clip_count)
         if clip_count.numel() < 1:
             raise ValueError("clip_count must have an element")
     _check(_lib.fh_kv_cache_write(cache._ref, k.data_ptr(), v.data_ptr(), n, ldk, ldv, slots.data_ptr(),
-                                  None if clip_count is None else clip_count.data_ptr(), _stream(stream)))
+                                  None if clip_count is None else clip_count.data_ptr(), _raw_stream(stream, index)))
 
 
 def fh_kv_cache_read(cache: KVCache, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
     """BF16 k, v [tokens, kv_heads, head_dim] = the cached values of slots (int64 [tokens]; rows of negative ones are
     left as they were)."""
-    _need_current(cache.device)
-    _need_all(cache.device, torch.int64, slots=slots)
+    index = cache.index
+    _need_current(index)
+    _need_all(index, torch.int64, "slots", slots)
     n = slots.numel()
     ldk, ldv = _kv_rows(cache, k, n, "k"), _kv_rows(cache, v, n, "v")
     _check(_lib.fh_kv_cache_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), ldk, ldv,
-                                 _stream(stream)))
+                                 _raw_stream(stream, index)))
 
 
 def fh_kv_attention_workspace_bytes(total_q: int, batch: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -594,20 +605,23 @@ def fh_kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     requests with query rows q_starts[b] .. q_starts[b + 1] - 1 and lens[b] cached tokens in the pages of block_table
     [batch, max_pages] (int32 all; see include/fh.h).  workspace: empty_kv_attention_workspace(...).  max_q, max_kv:
     upper bounds of a request's queries and cached tokens, which choose the kernel.  lse: FP32 [total_q, q_heads]."""
-    device = cache.device
-    _need_current(device)
-    _need(q, _BF16, "q", 3)
-    _need(out, _BF16, "out", 3)
-    _need_all(device, torch.int32, block_table=block_table, lens=lens, q_starts=q_starts)
-    _need_all(device, torch.uint8, workspace=workspace)
-    total_q, heads, d = q.shape
+    index = cache.index
+    _need_current(index)
+    for t, what in ((q, "q"), (out, "out")):
+        if not isinstance(t, torch.Tensor) or t.dtype not in _BF16:
+            raise TypeError(f"{what} must be a BF16 tensor")
+    _need_all(index, torch.int32, "block_table, lens, q_starts", block_table, lens, q_starts)
+    _need_all(index, torch.uint8, "workspace", workspace)
+    shape = q.shape
     n = lens.numel()
-    if (d != cache.head_dim or out.shape != q.shape or q.device != device or out.device != device
-            or q_starts.numel() != n + 1 or block_table.dim() != 2 or block_table.shape[0] != n):
+    if (len(shape) != 3 or shape[2] != cache.head_dim or out.shape != shape or q.get_device() != index
+            or out.get_device() != index or q_starts.numel() != n + 1 or block_table.dim() != 2
+            or block_table.shape[0] != n):
         raise ValueError("shape mismatch: q, out [total_q, q_heads, head_dim], lens [batch], q_starts [batch + 1], "
                          "block_table [batch, max_pages], on the cache's device")
+    total_q, heads, _ = shape
     if lse is not None:
-        _need_all(device, torch.float32, lse=lse)
+        _need_all(index, torch.float32, "lse", lse)
         if lse.shape != (total_q, heads):
             raise ValueError("lse must be [total_q, q_heads]")
     max_pages = block_table.shape[1]
@@ -616,7 +630,7 @@ def fh_kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
                                 window, total_q if max_q is None else max_q,
                                 max_pages * cache.page_size if max_kv is None else max_kv, out.data_ptr(),
                                 _row_stride(out, "out"), None if lse is None else lse.data_ptr(),
-                                workspace.data_ptr(), workspace.numel(), _stream(stream)))
+                                workspace.data_ptr(), workspace.numel(), _raw_stream(stream, index)))
 
 
 def fh_selftest_bounded_wait(limit_us: int, stream=None) -> None:

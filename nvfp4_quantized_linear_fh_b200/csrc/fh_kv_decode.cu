@@ -197,30 +197,39 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
     }
   }
   __syncthreads();
-  w.b = start_s[0];
-  load_walk(p, R, w);
-  w.tile = start_s[1];
-  w.head = start_s[2];
-  w.unit = start_s[3];
-  Walk f = w;  // the unit to fetch next
+  Walk f;  // the unit to fetch next
+  f.b = start_s[0];
+  load_walk(p, R, f);
+  f.tile = start_s[1];
+  f.head = start_s[2];
+  f.unit = start_s[3];
+  int at_b = f.b, at_tile = f.tile, at_head = f.head, at_unit = f.unit;  // the unit to work on
   long long n_left = u1 - u0, n_fetch = n_left;
   long long at = u0;  // the line's index of the current unit
 
   // --- fetching: this warp's 32 tokens of a unit into a stage ---------------------
+  // The pages of the unit to fetch are looked up one unit ahead.
+  int next_page[2];
+  auto look_up = [&]() {
+    const int tok0 = (f.u_lo + f.unit) * kUnit + warp * kWarpTokens;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // A group of 16 tokens lies in one page (page sizes are multiples of 16).
+      const int tok = tok0 + 16 * h;
+      next_page[h] = -1;
+      if (tok < f.rq.hi && tok + 16 > f.rq.lo) next_page[h] = p.table[(int64_t)f.b * p.max_pages + (tok >> p.page_shift)];
+    }
+  };
   auto fetch = [&](int stage) {
     const int tok0 = (f.u_lo + f.unit) * kUnit + warp * kWarpTokens;
     const uint32_t base = ring + stage * St::kBytes;
     const int ps = 1 << p.page_shift;
-    // Two groups of 16 tokens; each lies in one page (page sizes are multiples of 16).
     int64_t first[2];
     bool live[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int tok = tok0 + 16 * h;
-      int page = -1;
-      if (tok < f.rq.hi && tok + 16 > f.rq.lo) page = p.table[(int64_t)f.b * p.max_pages + (tok >> p.page_shift)];
-      live[h] = page >= 0 && page < p.num_pages;
-      first[h] = live[h] ? (((int64_t)page * p.kv_heads + f.head) << p.page_shift) + (tok & (ps - 1)) : 0;
+      live[h] = next_page[h] >= 0 && next_page[h] < p.num_pages;
+      first[h] = live[h] ? (((int64_t)next_page[h] * p.kv_heads + f.head) << p.page_shift) + ((tok0 + 16 * h) & (ps - 1)) : 0;
     }
     constexpr int kCpr = D / 32;                       // 16-byte chunks of a row of codes
     constexpr int kCodeCopies = kWarpTokens * kCpr / 32;
@@ -253,11 +262,15 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
     if (n_fetch > 0) {
       const uint32_t lv = fetch(fetch_stage);
       live_bits = (live_bits & ~(3u << (2 * fetch_stage))) | (lv << (2 * fetch_stage));
-      if (--n_fetch > 0) advance(p, R, f);
+      if (--n_fetch > 0) {
+        advance(p, R, f);
+        look_up();
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     fetch_stage = fetch_stage + 1 == kStages ? 0 : fetch_stage + 1;
   };
+  look_up();
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch_next();
   int stage = 0;
@@ -265,8 +278,11 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
   bool first_segment = true;
   while (n_left > 0) {
     // --- a segment: consecutive units of one tile ---------------------------------
-    const int seg_tile = w.tile, seg_head = w.head, seg_unit0 = w.unit, n_units = w.n_units;
+    w.b = at_b;
+    load_walk(p, R, w);
+    const int seg_tile = at_tile, seg_head = at_head, seg_unit0 = at_unit, n_units = w.n_units;
     const Request rq = w.rq;
+    const int seg_tok0 = (w.u_lo + seg_unit0) * kUnit + warp * kWarpTokens;
     const int seg_n = (int)min(n_left, (long long)(n_units - seg_unit0));
     const int n_rows = (int)min((int64_t)R, (int64_t)rq.n_q * p.group - (int64_t)seg_tile * R);
 
@@ -300,7 +316,8 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
       amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
       const int e = query_exponent(amax);
-      const float up = pow2(e);
+      // A negative scale goes to the query, so that larger scores are larger sums.
+      const float up = p.qk_scale < 0.0f ? -pow2(e) : pow2(e);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -310,7 +327,8 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int col = 2 * t + c, rr = nt * 8 + col;
-        factor[nt][c] = p.qk_scale * pow2(-__shfl_sync(0xFFFFFFFFu, e, 4 * col));
+        // Never 0: a hidden score of -inf stays -inf times it.
+        factor[nt][c] = fmaxf(fabsf(p.qk_scale) * pow2(-__shfl_sync(0xFFFFFFFFu, e, 4 * col)), 1.17549435e-38f);
         const int2 s = rr < n_rows ? seen_by(p, rq, (int)(((uint32_t)seg_tile * R + rr) / p.group)) : make_int2(0, rq.hi);
         lo_q[nt][c] = s.x;
         hi_q[nt][c] = s.y;
@@ -340,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();
       const uint8_t* sb = ring_p + stage * St::kBytes;
-      const int tok0 = (w.u_lo + seg_unit0 + u) * kUnit + warp * kWarpTokens;
+      const int tok0 = seg_tok0 + u * kUnit;
       const uint32_t lv = (live_bits >> (2 * stage)) & 3u;
       const bool edge = lv != 3u || tok0 < lo_max || tok0 + kWarpTokens > hi_min;
       if (lv != 0u && tok0 < rq.hi) {
@@ -399,13 +417,7 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
               mma_16816(s[i][nt], c0, c1, c2, c3, qf[nt][4 * wd + 2], qf[nt][4 * wd + 3]);
           }
         }
-        // --- to log2 units, masked ------------------------------------------------------
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) s[i][nt][c] *= factor[nt][c & 1];
+        // --- scores of tokens not seen ---------------------------------------------------
         if (edge) {
           const int tok_g = (g >> 1) + 4 * (g & 1);
 #pragma unroll
@@ -427,7 +439,8 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            top[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+            // In log2 units (the factor is > 0).
+            top[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2])) * factor[nt][c];
             raise = raise || top[nt][c] > m[nt][c] + kRaise;
           }
         if (__any_sync(0xFFFFFFFFu, raise)) {
@@ -458,8 +471,8 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
           const float off1 = m[nt][1] == -INFINITY ? 0.0f : kHead - m[nt][1];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float p0 = exp2_fast(s[i][nt][0] + off0), p1 = exp2_fast(s[i][nt][1] + off1);
-            const float p2 = exp2_fast(s[i][nt][2] + off0), p3 = exp2_fast(s[i][nt][3] + off1);
+            const float p0 = exp2_fast(fmaf(s[i][nt][0], factor[nt][0], off0)), p1 = exp2_fast(fmaf(s[i][nt][1], factor[nt][1], off1));
+            const float p2 = exp2_fast(fmaf(s[i][nt][2], factor[nt][0], off0)), p3 = exp2_fast(fmaf(s[i][nt][3], factor[nt][1], off1));
             l[nt][0] += p0 + p2;
             l[nt][1] += p1 + p3;
             pb[i][nt][0] = transpose8x8(pack_f16x2(p0, p1));
@@ -634,8 +647,9 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
     at += seg_n;
     n_left -= seg_n;
     if (n_left > 0) {
-      w.unit += seg_n - 1;
+      w.b = at_b, w.tile = at_tile, w.head = at_head, w.unit = at_unit + seg_n - 1;
       advance(p, R, w);
+      at_b = w.b, at_tile = w.tile, at_head = w.head, at_unit = w.unit;
     }
     __syncthreads();  // o_s and ml_s are written again by the next segment
   }
