@@ -11,8 +11,10 @@
 // on the other.  A thread has one 16-element block (32 bytes of BF16, 8 of
 // codes, one scale); the blocks of a token follow one another in the rows of
 // x, and the 64 code bytes of one head (d = 128) in the page, so both sides
-// move whole sectors.  Four blocks per thread are in flight at once.  Keys and
-// values go in one launch (blockIdx.y), each with its own decision table.
+// move whole sectors: a block's BF16 in one 256-bit access where rows are
+// 32-byte aligned, else in two of 128.  A thread has several blocks in flight,
+// their rows read beside the slots, not behind them.  Keys and values go
+// in one launch (blockIdx.y), each with its own decision table.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>
@@ -28,7 +30,10 @@ namespace {
 using namespace nvfp4;
 
 constexpr int kKvThreads = 256;
-constexpr int kKvBlocksPerThread = 4;
+// Blocks of a thread in flight.  32768 tokens x 21 heads x 128: write 87 us
+// with four in 64 registers (four CTAs an SM), 100 in 80 registers, 91 with
+// two; read 73 with two, 79 with four.
+constexpr int kWriteBlocks = 4, kReadBlocks = 2;
 
 // One of keys and values.
 struct KvSide {
@@ -48,6 +53,7 @@ struct KvParams {
   int64_t groups;           // of `group` tokens each
   int group;
   uint32_t row_blocks;      // kv_heads * d / 16
+  uint32_t step_tokens, step_blocks;  // kKvThreads blocks on, as whole rows and a rest
   int head_shift;           // log2(d / 16)
   int page_shift, kv_heads;
   unsigned long long* clip;
@@ -61,11 +67,56 @@ struct KvWriteParams {
 // Where the block `j` of a token's row lies: its index among the cache's blocks.
 __device__ __forceinline__ int64_t cache_block(const KvParams& p, int64_t slot, uint32_t j) {
   const uint32_t head = j >> p.head_shift, in_head = j & ((1u << p.head_shift) - 1);
-  const int64_t page = slot >> p.page_shift, at = slot & (((int64_t)1 << p.page_shift) - 1);
-  return (((page * p.kv_heads + head) << p.page_shift) + at) * ((int64_t)1 << p.head_shift) + in_head;
+  const int64_t page = slot >> p.page_shift;
+  const uint32_t at = (uint32_t)slot & ((1u << p.page_shift) - 1);
+  return ((page * p.kv_heads + head) << (p.page_shift + p.head_shift)) + ((at << p.head_shift) + in_head);
 }
 
-__global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_constant__ KvWriteParams wp) {
+// A block's 32 bytes.  kWide: one access of 256 bits (32-byte aligned).
+template <bool kWide>
+__device__ __forceinline__ void load_block(const uint16_t* x, uint32_t (&w)[8]) {
+  if constexpr (kWide) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(x));
+  } else {
+    const uint4 a = reinterpret_cast<const uint4*>(x)[0], b = reinterpret_cast<const uint4*>(x)[1];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+}
+
+template <bool kWide>
+__device__ __forceinline__ void store_block(uint16_t* y, const uint32_t (&w)[8]) {
+  if constexpr (kWide) {
+    asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "l"(y)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(y)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(y)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// A thread's blocks within a CTA's group of tokens: block i0 = its index, then
+// every kKvThreads-th, as (token, block of the row) without a division each.
+struct BlockWalk {
+  uint32_t t, j;
+  __device__ __forceinline__ BlockWalk(const KvParams& p) {
+    t = threadIdx.x / p.row_blocks;
+    j = threadIdx.x - t * p.row_blocks;
+  }
+  __device__ __forceinline__ void next(const KvParams& p) {
+    t += p.step_tokens;
+    j += p.step_blocks;
+    if (j >= p.row_blocks) {
+      j -= p.row_blocks;
+      ++t;
+    }
+  }
+};
+
+template <bool kWide>
+__global__ void __launch_bounds__(kKvThreads, 4) kv_write_kernel(const __grid_constant__ KvWriteParams wp) {
   __shared__ QuantTable tab;
   const KvParams& p = wp.k;
   const KvSide& s = p.side[blockIdx.y];
@@ -78,35 +129,31 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_const
   uint32_t clips = 0;
   for (int64_t g = blockIdx.x; g < p.groups; g += gridDim.x) {
     const int64_t t0 = g * p.group;
-    const uint32_t n = (uint32_t)min((int64_t)p.group, p.tokens - t0) * p.row_blocks;
-    for (uint32_t i0 = threadIdx.x; i0 < n; i0 += kKvThreads * kKvBlocksPerThread) {
-      uint4 q[kKvBlocksPerThread][2];
-      int64_t at[kKvBlocksPerThread];
+    const uint32_t n = (uint32_t)min((int64_t)p.group, p.tokens - t0);  // tokens
+    BlockWalk at(p);
+    while (at.t < n) {
+      uint32_t w[kWriteBlocks][8], j[kWriteBlocks];
+      int64_t slot[kWriteBlocks];
 #pragma unroll
-      for (int u = 0; u < kKvBlocksPerThread; ++u) {
-        const uint32_t i = i0 + u * kKvThreads;
-        at[u] = -1;
-        if (i < n) {
-          const uint32_t t = i / p.row_blocks, j = i - t * p.row_blocks;
-          const int64_t slot = p.slots[t0 + t];
-          if (slot >= 0 && slot < p.n_slots) {
-            at[u] = cache_block(p, slot, j);
-            const uint4* src = reinterpret_cast<const uint4*>(s.x + (t0 + t) * s.ld + 16 * (int64_t)j);
-            q[u][0] = __ldcs(src);
-            q[u][1] = __ldcs(src + 1);
-          }
+      for (int u = 0; u < kWriteBlocks; ++u) {
+        slot[u] = -1;
+        j[u] = at.j;
+        if (at.t < n) {
+          slot[u] = p.slots[t0 + at.t];
+          load_block<kWide>(s.x + (t0 + at.t) * s.ld + 16 * at.j, w[u]);
         }
+        at.next(p);
       }
 #pragma unroll
-      for (int u = 0; u < kKvBlocksPerThread; ++u) {
-        if (at[u] < 0) continue;
-        const uint32_t w[8] = {q[u][0].x, q[u][0].y, q[u][0].z, q[u][0].w, q[u][1].x, q[u][1].y, q[u][1].z, q[u][1].w};
+      for (int u = 0; u < kWriteBlocks; ++u) {
+        if (slot[u] < 0 || slot[u] >= p.n_slots) continue;
         uint32_t amax;
         uint2 codes;
-        const uint32_t c = quantize_block_codes(tab, s.inv6sg, w, amax, codes);
-        *reinterpret_cast<uint2*>(s.codes + 8 * at[u]) = codes;
-        s.scales[at[u]] = (uint8_t)c;
-        clips += block_clips(w, amax, s.clip_thr);
+        const uint32_t c = quantize_block_codes(tab, s.inv6sg, w[u], amax, codes);
+        const int64_t b = cache_block(p, slot[u], j[u]);
+        *reinterpret_cast<uint2*>(s.codes + 8 * b) = codes;
+        s.scales[b] = (uint8_t)c;
+        clips += block_clips(w[u], amax, s.clip_thr);
       }
     }
   }
@@ -116,39 +163,42 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_const
   }
 }
 
+template <bool kWide>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_constant__ KvParams p) {
   const KvSide& s = p.side[blockIdx.y];
+  const float2 gs = make_float2(s.gscale, s.gscale);
   for (int64_t g = blockIdx.x; g < p.groups; g += gridDim.x) {
     const int64_t t0 = g * p.group;
-    const uint32_t n = (uint32_t)min((int64_t)p.group, p.tokens - t0) * p.row_blocks;
-    for (uint32_t i0 = threadIdx.x; i0 < n; i0 += kKvThreads * kKvBlocksPerThread) {
-      uint2 codes[kKvBlocksPerThread];
-      uint32_t scale[kKvBlocksPerThread];
-      uint16_t* out[kKvBlocksPerThread];
+    const uint32_t n = (uint32_t)min((int64_t)p.group, p.tokens - t0);  // tokens
+    BlockWalk at(p);
+    while (at.t < n) {
+      int64_t slot[kReadBlocks];
+      uint32_t t[kReadBlocks], j[kReadBlocks], scale[kReadBlocks];
+      uint2 codes[kReadBlocks];
 #pragma unroll
-      for (int u = 0; u < kKvBlocksPerThread; ++u) {
-        const uint32_t i = i0 + u * kKvThreads;
-        out[u] = nullptr;
-        if (i < n) {
-          const uint32_t t = i / p.row_blocks, j = i - t * p.row_blocks;
-          const int64_t slot = p.slots[t0 + t];
-          if (slot >= 0 && slot < p.n_slots) {
-            const int64_t at = cache_block(p, slot, j);
-            codes[u] = *reinterpret_cast<const uint2*>(s.codes + 8 * at);
-            scale[u] = s.scales[at];
-            out[u] = s.y + (t0 + t) * s.ld + 16 * (int64_t)j;
-          }
-        }
+      for (int u = 0; u < kReadBlocks; ++u) {
+        slot[u] = at.t < n ? p.slots[t0 + at.t] : -1;
+        t[u] = at.t;
+        j[u] = at.j;
+        at.next(p);
       }
 #pragma unroll
-      for (int u = 0; u < kKvBlocksPerThread; ++u) {
-        if (out[u] == nullptr) continue;
-        const float sc = kv::f16x2_to_float2(kv::e4m3x2_to_f16x2(scale[u])).x;
-        uint32_t w[8];
-        auto word = [&](uint32_t f16x2) {
-          const float2 v = kv::f16x2_to_float2(f16x2);
-          return kv::pack_bf16x2((v.x * sc) * s.gscale, (v.y * sc) * s.gscale);
+      for (int u = 0; u < kReadBlocks; ++u) {
+        if (slot[u] < 0 || slot[u] >= p.n_slots) continue;
+        const int64_t b = cache_block(p, slot[u], j[u]);
+        codes[u] = *reinterpret_cast<const uint2*>(s.codes + 8 * b);
+        scale[u] = s.scales[b];
+      }
+#pragma unroll
+      for (int u = 0; u < kReadBlocks; ++u) {
+        if (slot[u] < 0 || slot[u] >= p.n_slots) continue;
+        const uint32_t h = kv::e4m3x2_to_f16x2(scale[u]);
+        const uint32_t sc = __byte_perm(h, h, 0x1010);
+        auto word = [&](uint32_t pair) {  // code * scale is exact in FP16
+          const float2 v = __fmul2_rn(kv::f16x2_to_float2(kv::hmul2(pair, sc)), gs);
+          return kv::pack_bf16x2(v.x, v.y);
         };
+        uint32_t w[8];
         w[0] = word(kv::e2m1x2_to_f16x2<0>(codes[u].x));
         w[1] = word(kv::e2m1x2_to_f16x2<1>(codes[u].x));
         w[2] = word(kv::e2m1x2_to_f16x2<2>(codes[u].x));
@@ -157,8 +207,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_consta
         w[5] = word(kv::e2m1x2_to_f16x2<1>(codes[u].y));
         w[6] = word(kv::e2m1x2_to_f16x2<2>(codes[u].y));
         w[7] = word(kv::e2m1x2_to_f16x2<3>(codes[u].y));
-        reinterpret_cast<uint4*>(out[u])[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(out[u])[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        store_block<kWide>(s.y + (t0 + t[u]) * s.ld + 16 * j[u], w);
       }
     }
   }
@@ -170,11 +219,13 @@ int log2_of(int64_t v) {
   return s;
 }
 
-void fill_params(KvParams* p, const fh_kv_cache& c, const int64_t* slots, int64_t tokens) {
+void fill_params(KvParams* p, const fh_kv_cache& c, const int64_t* slots, int64_t tokens, int per_thread) {
   p->slots = slots;
   p->tokens = tokens;
   p->n_slots = c.num_pages * c.page_size;
   p->row_blocks = (uint32_t)(c.kv_heads * c.head_dim / 16);
+  p->step_tokens = kKvThreads / p->row_blocks;
+  p->step_blocks = kKvThreads % p->row_blocks;
   p->head_shift = log2_of(c.head_dim / 16);
   p->page_shift = log2_of(c.page_size);
   p->kv_heads = (int)c.kv_heads;
@@ -187,17 +238,20 @@ void fill_params(KvParams* p, const fh_kv_cache& c, const int64_t* slots, int64_
     p->side[i].scales = scales[i];
     p->side[i].gscale = gs[i];
   }
-  // A group is what a CTA takes at a time: about a thousand blocks, so that
-  // each thread has four, and at least one token.
-  const int64_t blocks = (int64_t)kKvThreads * kKvBlocksPerThread;
+  // A group is what a CTA takes at a time: per_thread blocks a thread or a few
+  // less, and at least one token.
+  const int64_t blocks = (int64_t)kKvThreads * per_thread;
   p->group = (int)(blocks / p->row_blocks > 0 ? blocks / p->row_blocks : 1);
   p->groups = (tokens + p->group - 1) / p->group;
 }
 
-dim3 kv_grid(const KvParams& p) {
-  const int64_t cap = (int64_t)sm_count() * 4;
+dim3 kv_grid(const KvParams& p, int per_sm) {
+  const int64_t cap = (int64_t)sm_count() * per_sm;
   return dim3((unsigned)(p.groups < cap ? p.groups : cap), 2);
 }
+
+// Whether every block of 16 elements of these rows is 32-byte aligned.
+bool wide_rows(const uint16_t* x, int64_t ld) { return (reinterpret_cast<uintptr_t>(x) & 31) == 0 && ld % 16 == 0; }
 
 }  // namespace
 
@@ -206,7 +260,7 @@ cudaError_t launch_kv_write(const fh_kv_cache& c, const uint16_t* k, const uint1
   KvWriteParams p;
   memcpy(&p.tab[0], &quant_table_for(c.k_gscale), sizeof(QuantTable));
   memcpy(&p.tab[1], &quant_table_for(c.v_gscale), sizeof(QuantTable));
-  fill_params(&p.k, c, slots, tokens);
+  fill_params(&p.k, c, slots, tokens, kWriteBlocks);
   p.k.clip = clip;
   const uint16_t* x[2] = {k, v};
   const int64_t ld[2] = {ldk, ldv};
@@ -218,14 +272,17 @@ cudaError_t launch_kv_write(const fh_kv_cache& c, const uint16_t* k, const uint1
     e.inv6sg = (float)(1.0 / (6.0 * (double)e.gscale));
     e.clip_thr = clip_threshold_bits(e.gscale);
   }
-  kv_write_kernel<<<kv_grid(p.k), kKvThreads, 0, s>>>(p);
+  if (wide_rows(k, ldk) && wide_rows(v, ldv))
+    kv_write_kernel<true><<<kv_grid(p.k, 2), kKvThreads, 0, s>>>(p);
+  else
+    kv_write_kernel<false><<<kv_grid(p.k, 2), kKvThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read(const fh_kv_cache& c, const int64_t* slots, int64_t tokens, uint16_t* k, uint16_t* v,
                            int64_t ldk, int64_t ldv, cudaStream_t s) {
   KvParams p;
-  fill_params(&p, c, slots, tokens);
+  fill_params(&p, c, slots, tokens, kReadBlocks);
   uint16_t* y[2] = {k, v};
   const int64_t ld[2] = {ldk, ldv};
   for (int i = 0; i < 2; ++i) {
@@ -235,7 +292,10 @@ cudaError_t launch_kv_read(const fh_kv_cache& c, const int64_t* slots, int64_t t
     p.side[i].inv6sg = 0.0f;
     p.side[i].clip_thr = 0;
   }
-  kv_read_kernel<<<kv_grid(p), kKvThreads, 0, s>>>(p);
+  if (wide_rows(k, ldk) && wide_rows(v, ldv))
+    kv_read_kernel<true><<<kv_grid(p, 16), kKvThreads, 0, s>>>(p);
+  else
+    kv_read_kernel<false><<<kv_grid(p, 16), kKvThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 

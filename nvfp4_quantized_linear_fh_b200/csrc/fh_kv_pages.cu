@@ -9,14 +9,18 @@
 // pages taken, new tokens) place every entry and every slot independently of
 // the others, so each output is written once, by whichever thread has it.
 //
-// One cluster of eight CTAs, whose hardware barrier separates reading the
-// lengths and the stack's count from overwriting them: the outputs may be the
-// inputs' own buffers, and no workspace, counter or second launch is needed.
-// Every CTA forms the prefix sums of all requests for itself in shared memory
-// (that is cheaper than exchanging them); a warp then takes 128 consecutive
+// The tables are one cluster's work (one CTA for small calls, eight for large
+// ones), whose hardware barrier separates reading the lengths and the stack's
+// count from overwriting them: the outputs may be the inputs' own buffers, and
+// no workspace or counter is needed.  Every CTA forms the prefix sums of all
+// requests for itself in shared memory (that is cheaper than exchanging them).
+// Few slots are written by the same launch.  Many go to a second one over the
+// whole GPU, which needs only the first one's outputs: a growing request held
+// lens - (q_starts[b + 1] - q_starts[b]) tokens.  A warp takes 128 consecutive
 // slots, finds the requests of the first and the last by binary search, and its
-// lanes search only between those.  The call is latency-bound: it moves a few
-// bytes a request and eight a slot.
+// lanes search only between those.  Bound by latency: a call moves a few bytes
+// a request and eight a slot.  (All in one cluster of eight, 300,000 slots
+// took 45 us.)
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -27,8 +31,10 @@ namespace fh {
 
 namespace {
 
-constexpr int kPagesCtas = 8;
+constexpr int kPagesCtas = 8;      // of a large call's cluster
 constexpr int kPagesThreads = 1024;
+constexpr int kFewSlots = 8192;    // written by the first launch
+constexpr int kRun = 128;          // slots a warp takes at a time
 
 struct PagesParams {
   const int32_t* held;
@@ -57,8 +63,38 @@ __device__ __forceinline__ int owner_of(const int32_t* a, int lo, int hi, int x)
   return lo;
 }
 
-__global__ void __cluster_dims__(kPagesCtas, 1, 1) __launch_bounds__(kPagesThreads, 1)
-    kv_pages_kernel(const PagesParams p) {
+// The slots of this thread's share of [0, capacity): page_of(b, at) names the
+// page of request b's table entry `at`, start(b) where its new tokens begin.
+template <class Held, class PageOf>
+__device__ __forceinline__ void write_slots(const PagesParams& p, const int32_t* starts, int n_rows, int64_t warp,
+                                            int64_t warps, Held held, PageOf page_of) {
+  const int lane = threadIdx.x & 31, n = p.batch;
+  for (int64_t r0 = warp * kRun; r0 < p.slot_capacity; r0 += warps * kRun) {
+    int first = 0, last = 0;
+    if (r0 < n_rows) {
+      const int x = lane == 0 ? (int)r0 : (int)min(r0 + kRun - 1, (int64_t)n_rows - 1);
+      const int b = owner_of(starts, 0, n, x);
+      first = __shfl_sync(0xFFFFFFFFu, b, 0);
+      last = __shfl_sync(0xFFFFFFFFu, b, 1);
+    }
+#pragma unroll
+    for (int k = 0; k < kRun / 32; ++k) {
+      const int64_t r = r0 + k * 32 + lane;
+      if (r >= p.slot_capacity) break;
+      int64_t slot = -1;
+      if (r < n_rows) {
+        const int b = owner_of(starts, first, last + 1, (int)r);
+        const int token = held(b) + ((int)r - starts[b]);
+        const int page = page_of(b, token >> p.shift);
+        if (page >= 0) slot = ((int64_t)page << p.shift) + (token & ((1 << p.shift) - 1));
+      }
+      p.slots[r] = slot;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kPagesThreads, 1) kv_pages_kernel(const PagesParams p, bool with_slots) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ int32_t pages_smem[];
   const int n = p.batch;
   int32_t* held_s = pages_smem;          // [n]
@@ -66,7 +102,7 @@ __global__ void __cluster_dims__(kPagesCtas, 1, 1) __launch_bounds__(kPagesThrea
   int32_t* taken = target_s + n;         // [n + 1] prefix sums, exclusive; [n] the total
   int32_t* given = taken + n + 1;        // [n + 1]
   int32_t* starts = given + n + 1;       // [n + 1]
-  __shared__ long long warp_sums[3][kPagesThreads / 32];
+  __shared__ long long warp_sums[3][kPagesThreads / 32 + 1];  // then their exclusive prefix, and the total
   __shared__ int bad_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto cluster = cooperative_groups::this_cluster();
@@ -110,13 +146,23 @@ __global__ void __cluster_dims__(kPagesCtas, 1, 1) __launch_bounds__(kPagesThrea
     if (lane == 31) warp_sums[k][warp] = v;
   }
   __syncthreads();
-  long long total[3] = {0, 0, 0};
+  if (warp < 3) {  // a warp a sum
+    const long long own = warp_sums[warp][lane];
+    long long v = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += u;
+    }
+    warp_sums[warp][lane] = v - own;
+    if (lane == 31) warp_sums[warp][32] = v;
+  }
+  __syncthreads();
+  long long total[3];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    for (int w = 0; w < kPagesThreads / 32; ++w) {
-      if (w < warp) pre[k] += warp_sums[k][w];
-      total[k] += warp_sums[k][w];
-    }
+    pre[k] += warp_sums[k][warp];
+    total[k] = warp_sums[k][32];
   }
   int status = bad_s;
   if (count < 0 || count + total[1] > p.free_capacity) status |= FH_KV_STACK_OVERFLOW;
@@ -142,9 +188,9 @@ __global__ void __cluster_dims__(kPagesCtas, 1, 1) __launch_bounds__(kPagesThrea
   cluster.sync();  // every CTA has read the lengths and the count: they may be overwritten
 
   const int gt = (int)cluster.block_rank() * kPagesThreads + tid;
-  constexpr int kAll = kPagesCtas * kPagesThreads;
+  const int all = (int)cluster.num_blocks() * kPagesThreads;
   const bool ok = status == 0;
-  for (int b = gt; b <= n; b += kAll) {
+  for (int b = gt; b <= n; b += all) {
     if (b < n) p.lens[b] = ok ? target_s[b] : held_s[b];
     p.q_starts[b] = ok ? starts[b] : 0;
   }
@@ -153,7 +199,8 @@ __global__ void __cluster_dims__(kPagesCtas, 1, 1) __launch_bounds__(kPagesThrea
     *p.status = status;
   }
   if (!ok) {
-    for (int64_t r = gt; r < p.slot_capacity; r += kAll) p.slots[r] = -1;
+    if (with_slots)
+      for (int64_t r = gt; r < p.slot_capacity; r += all) p.slots[r] = -1;
     return;
   }
   // The f-th page given back, from the entries behind its request's new end.
@@ -167,36 +214,32 @@ __global__ void __cluster_dims__(kPagesCtas, 1, 1) __launch_bounds__(kPagesThrea
     const int at = count + n_given - 1 - i;
     return at >= count ? given_page(at - count) : p.free_pages[at];
   };
-  for (int i = gt; i < n_taken; i += kAll) {
+  for (int i = gt; i < n_taken; i += all) {
     const int b = owner_of(taken, 0, n, i);
     p.table[(int64_t)b * p.max_pages + pages_of(held_s[b]) + (i - taken[b])] = taken_page(i);
   }
-  for (int f = gt; f < n_given; f += kAll) p.free_pages[(int64_t)count + f] = given_page(f);
+  for (int f = gt; f < n_given; f += all) p.free_pages[(int64_t)count + f] = given_page(f);
 
-  constexpr int kRun = 128;  // slots a warp takes at a time
-  for (int64_t r0 = (int64_t)(gt >> 5) * kRun; r0 < p.slot_capacity; r0 += (int64_t)(kAll / 32) * kRun) {
-    int first = 0, last = 0;
-    if (r0 < n_rows) {
-      const int x = lane == 0 ? (int)r0 : min((int)r0 + kRun - 1, n_rows - 1);
-      const int b = owner_of(starts, 0, n, x);
-      first = __shfl_sync(0xFFFFFFFFu, b, 0);
-      last = __shfl_sync(0xFFFFFFFFu, b, 1);
-    }
-#pragma unroll
-    for (int k = 0; k < kRun / 32; ++k) {
-      const int64_t r = r0 + k * 32 + lane;
-      if (r >= p.slot_capacity) break;
-      int64_t slot = -1;
-      if (r < n_rows) {
-        const int b = owner_of(starts, first, last + 1, (int)r);
-        const int token = held_s[b] + ((int)r - starts[b]);
-        const int at = token >> p.shift, have = pages_of(held_s[b]);
-        const int page = at < have ? p.table[(int64_t)b * p.max_pages + at] : taken_page(taken[b] + at - have);
-        if (page >= 0) slot = ((int64_t)page << p.shift) + (token & mask);
-      }
-      p.slots[r] = slot;
-    }
-  }
+  if (with_slots)
+    write_slots(p, starts, n_rows, gt >> 5, all / 32, [&](int b) { return held_s[b]; },
+                [&](int b, int at) {
+                  const int have = pages_of(held_s[b]);
+                  return at < have ? p.table[(int64_t)b * p.max_pages + at] : taken_page(taken[b] + at - have);
+                });
+}
+
+constexpr int kSlotThreads = 512;
+
+// The slots alone, from what kv_pages_kernel has written.
+__global__ void __launch_bounds__(kSlotThreads) kv_slots_kernel(const PagesParams p) {
+  extern __shared__ int32_t pages_smem[];  // [batch + 1]
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int b = threadIdx.x; b <= p.batch; b += kSlotThreads) pages_smem[b] = p.q_starts[b];
+  __syncthreads();
+  const int32_t* starts = pages_smem;
+  write_slots(p, starts, starts[p.batch], ((int64_t)blockIdx.x * kSlotThreads + threadIdx.x) >> 5,
+              (int64_t)gridDim.x * (kSlotThreads / 32), [&](int b) { return p.lens[b] - (starts[b + 1] - starts[b]); },
+              [&](int b, int at) { return p.table[(int64_t)b * p.max_pages + at]; });
 }
 
 }  // namespace
@@ -232,8 +275,34 @@ cudaError_t launch_kv_pages(const int32_t* held, const int32_t* target, int64_t 
     return e == cudaSuccess ? 1 : -(int)e;
   });
   if (cfg <= 0) return (cudaError_t)(-cfg);
-  kv_pages_kernel<<<kPagesCtas, kPagesThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  const bool few = slot_capacity <= kFewSlots;
+  // Table entries to write: at most one a request and one a page of new tokens.
+  const bool large = batch + slot_capacity / page_size > 1024;
+  cudaLaunchConfig_t cfg_a = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = large ? kPagesCtas : 1;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg_a.gridDim = dim3(large ? kPagesCtas : 1);
+  cfg_a.blockDim = dim3(kPagesThreads);
+  cfg_a.dynamicSmemBytes = smem;
+  cfg_a.stream = s;
+  cfg_a.attrs = attr;
+  cfg_a.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg_a, kv_pages_kernel, p, few);
+  if (e != cudaSuccess || few) return e;
+  const int64_t runs = (slot_capacity + kRun - 1) / kRun, per_cta = kSlotThreads / 32;
+  const int64_t want = (runs + per_cta - 1) / per_cta, cap = (int64_t)sm_count() * 4;
+  cudaLaunchConfig_t cfg_b = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg_b.gridDim = dim3((unsigned)(want < cap ? want : cap));
+  cfg_b.blockDim = dim3(kSlotThreads);
+  cfg_b.dynamicSmemBytes = (size_t)(batch + 1) * 4;
+  cfg_b.stream = s;
+  cfg_b.attrs = attr;
+  cfg_b.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg_b, kv_slots_kernel, p);
 }
 
 }  // namespace fh

@@ -82,6 +82,31 @@ def test_slices_of_the_fused_qkv_rows():
     check(301, 21, 128, 64, 9, dev=dev)
 
 
+@pytest.mark.parametrize("off,ld", [(8, 528), (0, 520), (16, 544), (8, 1000)])
+def test_rows_of_sixteen_byte_alignment(off, ld):
+    """Rows that are 16-byte but not 32-byte aligned, and such that are, inside wider ones; read back likewise."""
+    m = fh()
+    T, H, d = 45, 4, 128
+    kb, vb = rows(T, H, d, off), rows(T, H, d, ld)
+    wide = [torch.full((T * ld + 64,), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    k, v, ko, vo = (w[off:off + T * ld].view(T, ld)[:, :H * d].unflatten(1, (H, d)) for w in wide)
+    k.copy_(to_dev(kb.reshape(T, -1)).view(T, H, d))
+    v.copy_(to_dev(vb.reshape(T, -1)).view(T, H, d))
+    cache = m.empty_kv_cache(4, 16, H, d, 0.003, 0.005)
+    slots = torch.randperm(64, device="cuda")[:T]
+    slots[7] = -1
+    m.fh_kv_cache_write(cache, k, v, slots)
+    m.fh_kv_cache_read(cache, slots, ko, vo)
+    keep = (slots >= 0).cpu().numpy()
+    for xb, back, w, sg in ((kb, ko, wide[2], 0.003), (vb, vo, wide[3], 0.005)):
+        oc, osc, _ = oracle.quantize(xb.reshape(-1, d), float(np.float32(sg)))
+        want = dequantize(oc, osc, 1.0).astype(np.float32) * np.float32(sg)
+        want = np.where(keep[:, None], S.to_bf16_bits(want).reshape(T, H * d), 0x4040)
+        np.testing.assert_array_equal(bits_of(back.contiguous()).reshape(T, -1), want)
+        back.fill_(3.0)
+        assert (w == 3.0).all(), "something beside the rows was written"
+
+
 def test_edge_values():
     """Zero blocks and negative zeros, a block that underflows the scale format, ties, clipped blocks, huge values."""
     x = np.zeros((8, 2, 64))

@@ -110,6 +110,21 @@ def test_refused_steps_leave_everything_as_it_was(alias):
     assert check(held, big, table, free, count, 16, 64, alias)[0] & m.FH_KV_TABLE_FULL
 
 
+@pytest.mark.parametrize("cap", [8192, 8193, 40000])
+def test_slots_of_one_launch_and_of_two(cap):
+    """Capacities at the border of the one-launch form; served, refused, and with no new token at all."""
+    rng = np.random.default_rng(cap)
+    held, target = mixed(rng, 300, 16, 400, 40)
+    need = int(np.maximum(-(-target // 16) - -(-held // 16), 0).sum())
+    table, free, count = start(rng, 300, 16, held, need, target=target)
+    assert check(held, target, table, free, count, 16, cap, True)[0] == 0
+    assert check(held, held + 17, table, free, 5, 16, cap, True)[0] == fh().FH_KV_NO_PAGES  # 300 pages and more, of 5
+    assert check(held, held, table, free, count, 16, cap, True)[0] == 0
+    held, target = np.array([10, 3, 7]), np.array([10 + cap - 5, 0, 7 + 5])  # the capacity to the last slot
+    table, free, count = start(rng, 3, 16, held, cap // 16 + 3, target=target)
+    assert check(held, target, table, free, count, 16, cap)[0] == 0
+
+
 def test_no_new_tokens_and_no_slots():
     rng = np.random.default_rng(4)
     held = np.array([3, 40, 0])
