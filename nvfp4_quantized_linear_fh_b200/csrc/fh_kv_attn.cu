@@ -6,7 +6,10 @@
 
 namespace fh {
 
-size_t kv_attention_workspace(const KvAttnShape& s) { return kv_attn_split_workspace(s); }
+size_t kv_attention_workspace(const KvAttnShape& s) {
+  const size_t a = kv_attn_split_workspace(s), b = kv_attn_tiles_workspace(s);
+  return a > b ? a : b;
+}
 
 cudaError_t launch_kv_attention(const fh_kv_cache& c, const KvAttnCall& call, const KvAttnShape& shape,
                                 void* workspace, cudaStream_t s) {
@@ -39,7 +42,7 @@ cudaError_t launch_kv_attention(const fh_kv_cache& c, const KvAttnCall& call, co
   p.part_o = nullptr;
   p.part_ml = nullptr;
   p.count = nullptr;
-  if (shape.max_q * p.group > 16) return launch_kv_attn_tiles(p, shape, s);
+  if (shape.max_q * p.group > kFewRows) return launch_kv_attn_tiles(p, shape, workspace, s);
   return launch_kv_attn_split(p, shape, workspace, s);
 }
 

@@ -63,11 +63,19 @@ __device__ __forceinline__ int2 seen_by(const AttnParams& p, const Request& r, i
 
 }  // namespace kv
 
+// Both kernels' workspace begins with this many counters, zero between calls;
+// nothing else is ever kept there.
+constexpr int kCounters = 1024;
+
+// Up to this many rows (queries x heads of a group) a request go to the kernel for few rows.
+constexpr int64_t kFewRows = 16;
+
 // Few rows a request (fh_kv_decode.cu).
 size_t kv_attn_split_workspace(const KvAttnShape& s);
 cudaError_t launch_kv_attn_split(const kv::AttnParams& p, const KvAttnShape& shape, void* workspace, cudaStream_t s);
 
 // Tiles of many rows, on the tcgen05 tensor cores (fh_kv_prefill.cu).
-cudaError_t launch_kv_attn_tiles(const kv::AttnParams& p, const KvAttnShape& shape, cudaStream_t s);
+size_t kv_attn_tiles_workspace(const KvAttnShape& s);
+cudaError_t launch_kv_attn_tiles(const kv::AttnParams& p, const KvAttnShape& shape, void* workspace, cudaStream_t s);
 
 }  // namespace fh

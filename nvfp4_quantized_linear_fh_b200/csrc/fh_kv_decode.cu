@@ -55,7 +55,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kUnit = 128;                  // tokens of a unit
 constexpr int kWarpTokens = kUnit / kWarps; // 32
 constexpr int kStages = 3;
-constexpr int kMaxCtas = 1024;              // workspace bound: two partial tiles per CTA
+constexpr int kMaxCtas = kCounters;         // workspace bound: a counter and two partial tiles per CTA
 constexpr float kRaise = 8.0f;              // log2: how far a score may exceed the running maximum
 constexpr float kHead = 6.0f;               // log2: head room of P above 1
 

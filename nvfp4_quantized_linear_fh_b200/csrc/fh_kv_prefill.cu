@@ -26,6 +26,11 @@
 // more than 8 (in log2), by the row's own thread: the commit that announces
 // S(j) also covers O += P(j-1) V, so nothing else is writing O then.
 //
+// Few rows over many keys (too few tiles for the GPU): the key tiles of a row
+// tile are cut into up to eight pieces, a CTA each, which leave their partial
+// results in the workspace; the one that finishes last (an atomic count; nobody
+// waits) joins them in the pieces' order.
+//
 // Queries, probabilities, sums and roundings are as in fh_kv_decode.cu.  Every
 // mbarrier wait is bounded; on expiry the kernel sets its error word, drains
 // what it issued, frees its TMEM and returns.
@@ -58,6 +63,8 @@ constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups: two warps of
 // eight softmax warps take 176, the others keep 80: 256 * 176 + 256 * 80 = 65536.
 constexpr int kSoftRegs = 176, kOtherRegs = 80;
 constexpr int kLive = 4;       // ring of the key tiles' page masks
+constexpr int kMaxPieces = 8;  // of a row tile's keys
+constexpr int kMaxPieceCtas = 320;  // workspace bound: a partial result each
 constexpr float kRaise = 8.0f;
 constexpr float kHead = 6.0f;
 
@@ -261,7 +268,8 @@ struct Job {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_prefill_kernel(const __grid_constant__ AttnParams p, int pieces) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -284,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
   int* job_s = reinterpret_cast<int*>(smem + C::kOffMisc + 16);  // request, tile
   __shared__ int scan_s[kThreads / 32];
+  __shared__ int last_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // --- which request and rows: the tiles of all requests in one line, the last
@@ -309,7 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
     if (i < warp) before += scan_s[i];
     total += scan_s[i];
   }
-  const int slot = total - 1 - (int)(blockIdx.x / p.kv_heads);
+  const int unit = (int)blockIdx.x / pieces, piece = (int)blockIdx.x % pieces;  // a row tile of a KV head, and which keys
+  const int slot = total - 1 - unit / p.kv_heads;
   if (slot < 0) return;
   if (slot >= before && slot < before + mine) {
     int rest = slot - before;
@@ -356,15 +366,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
   const uint32_t tmem = *tmem_slot;
   Job job;
   job.b = job_s[0];
-  job.head = (int)(blockIdx.x % p.kv_heads);
+  job.head = unit % p.kv_heads;
   job.rq = load_request(p, job.b);
   job.row0 = job_s[1] * kCtaRows;
   job.n_rows = (int)min((int64_t)kCtaRows, (int64_t)job.rq.n_q * p.group - job.row0);
   {
     const int lo = seen_by(p, job.rq, job.row0 / p.group).x;
     const int hi = seen_by(p, job.rq, (job.row0 + job.n_rows - 1) / p.group).y;
-    job.key0 = lo / kKeys;
-    job.n_keys = max(0, (hi + kKeys - 1) / kKeys - job.key0);
+    const int first = lo / kKeys, n = max(0, (hi + kKeys - 1) / kKeys - first);
+    const int from = (int)((int64_t)n * piece / pieces), to = (int)((int64_t)n * (piece + 1) / pieces);
+    job.key0 = first + from;
+    job.n_keys = to - from;
   }
   const int tiles = job.n_rows > kRows ? 2 : 1;
 
@@ -508,6 +520,52 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
       l = sum.x + sum.y;
       if (ok && job.n_keys > 0) ok = warp_wait(ofull(t), 0, abort_flag);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      float weight[kMaxPieces];  // of the pieces' partial outputs
+      if (pieces > 1) {  // (also when a wait has run out: all of these warps meet at the barriers)
+        // Partial results, column by column: a warp's 32 rows lie together.
+        float* part = p.part_o + (int64_t)blockIdx.x * (kCtaRows * D) + row;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          if (ok && job.n_keys > 0) {
+            tmem_load_32(to + 32 * c, v);
+            tmem_wait_32(v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) part[(32 * c + i) * kCtaRows] = __uint_as_float(v[i]);
+        }
+        p.part_ml[(int64_t)blockIdx.x * kCtaRows + row] = make_float2(m, l);
+        __threadfence();
+        asm volatile("bar.sync 1, %0;" ::"r"(kRows * tiles) : "memory");  // the softmax warps that have rows
+        if (tid == 0) {
+          last_s = atomicAdd(p.count + unit, 1u) == (unsigned)(pieces - 1);
+          if (last_s) p.count[unit] = 0;  // as the next call needs it
+        }
+        asm volatile("bar.sync 1, %0;" ::"r"(kRows * tiles) : "memory");
+        ok = ok && last_s != 0;  // the others are done
+        if (ok) {
+          __threadfence();
+          const float2* ml = p.part_ml + (int64_t)unit * pieces * kCtaRows + row;
+          float ms[kMaxPieces], ls[kMaxPieces];
+          m = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < kMaxPieces; ++i) {
+            const float2 x = i < pieces ? __ldcg(ml + i * kCtaRows) : make_float2(-INFINITY, 0.0f);
+            ms[i] = x.x;
+            ls[i] = x.y;
+            m = fmaxf(m, x.x);
+          }
+          l = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kMaxPieces; ++i) {
+            weight[i] = ms[i] == m ? 1.0f : exp2_fast(ms[i] - m);
+            l += weight[i] * ls[i];
+          }
+        }
+      }
       if (ok) {
         const float inv = l > 0.0f ? p.v_gscale / l : (l == 0.0f ? 0.0f : l);
         // Through shared memory (this warp's part of its Q tile, which the products
@@ -516,7 +574,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
-          if (job.n_keys > 0) {
+          if (pieces > 1) {
+            const float* part = p.part_o + (int64_t)unit * pieces * (kCtaRows * D) + (32 * c) * kCtaRows + row;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0;
+#pragma unroll 1
+            for (int k = 0; k < pieces; ++k) {
+              float w = weight[0];  // weight[k], without indexing registers
+#pragma unroll
+              for (int i = 1; i < kMaxPieces; ++i) w = k == i ? weight[i] : w;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                v[i] = __float_as_uint(
+                    fmaf(w, __ldcg(part + (int64_t)k * (kCtaRows * D) + i * kCtaRows), __uint_as_float(v[i])));
+            }
+          } else if (job.n_keys > 0) {
             tmem_load_32(to + 32 * c, v);
             tmem_wait_32(v);
           } else {
@@ -724,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const __grid_co
 }
 
 template <int D>
-cudaError_t launch_prefill(const AttnParams& p, int64_t grid, cudaStream_t s) {
+cudaError_t launch_prefill(const AttnParams& p, int64_t units, int pieces, cudaStream_t s) {
   using C = Cfg<D>;
   static DeviceTable configured;
   int dev = 0;
@@ -735,17 +807,52 @@ cudaError_t launch_prefill(const AttnParams& p, int64_t grid, cudaStream_t s) {
     return e == cudaSuccess ? 1 : -(int)e;
   });
   if (cfg <= 0) return (cudaError_t)(-cfg);
-  kv_prefill_kernel<D><<<(unsigned)grid, kThreads, C::kSmem, s>>>(p);
+  kv_prefill_kernel<D><<<(unsigned)(units * pieces), kThreads, C::kSmem, s>>>(p, pieces);
   return cudaGetLastError();
+}
+
+// As many row tiles (of all KV heads) as there can be: a request's last one may be short.
+int64_t most_units(const KvAttnShape& shape) {
+  const int64_t rows = shape.total_q * (shape.q_heads / shape.kv_heads), most = rows < shape.batch ? rows : shape.batch;
+  return (rows / (kRows * kTiles) + most) * shape.kv_heads;
+}
+
+// Into how many pieces the keys of a row tile are cut: as many as shorten the
+// call, a CTA taking about as long as three key tiles to start and finish and
+// the join of pieces as long as two more.
+int pieces_for(int64_t units, int64_t max_kv, int window, int sms) {
+  if (units >= sms) return 1;
+  if (window > 0 && max_kv > (int64_t)window + kRows * kTiles) max_kv = (int64_t)window + kRows * kTiles;
+  const int64_t keys = (max_kv + kKeys - 1) / kKeys;
+  int best = 1;
+  int64_t best_cost = keys + 3;
+  for (int n = 2; n <= kMaxPieces && units * n <= kMaxPieceCtas; ++n) {
+    const int64_t cost = (units * n + sms - 1) / sms * ((keys + n - 1) / n + 3) + 2;
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = n;
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attn_tiles(const AttnParams& p, const KvAttnShape& shape, cudaStream_t s) {
-  // As many CTAs as there can be tiles: a request's last tile may be short.
-  const int64_t rows = shape.total_q * p.group, most = rows < shape.batch ? rows : shape.batch;
-  const int64_t grid = (rows / (kRows * kTiles) + most) * shape.kv_heads;
-  return shape.head_dim == 128 ? launch_prefill<128>(p, grid, s) : launch_prefill<64>(p, grid, s);
+size_t kv_attn_tiles_workspace(const KvAttnShape& s) {
+  const int64_t units = most_units(s), ctas = units * kMaxPieces < kMaxPieceCtas ? units * kMaxPieces : kMaxPieceCtas;
+  if (s.total_q * (s.q_heads / s.kv_heads) <= kFewRows) return 0;  // never comes here
+  // (No less for more units, of which none is cut: a workspace serves smaller calls too.)
+  return kCounters * sizeof(unsigned) + (size_t)ctas * (kRows * kTiles) * (size_t)(s.head_dim + 2) * sizeof(float);
+}
+
+cudaError_t launch_kv_attn_tiles(const AttnParams& params, const KvAttnShape& shape, void* workspace, cudaStream_t s) {
+  AttnParams p = params;
+  const int64_t units = most_units(shape);
+  const int pieces = pieces_for(units, shape.max_kv, p.window, sm_count());
+  p.count = static_cast<unsigned*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.count + kCounters);
+  p.part_o = reinterpret_cast<float*>(p.part_ml + units * pieces * (kRows * kTiles));
+  return shape.head_dim == 128 ? launch_prefill<128>(p, units, pieces, s) : launch_prefill<64>(p, units, pieces, s);
 }
 
 cudaError_t read_and_clear_kv_error(unsigned int* bits) {

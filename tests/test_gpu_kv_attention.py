@@ -175,6 +175,30 @@ def test_long_lines_split_over_many_ctas(Hq, Hk, n_q):
     c.check(window=1500)
 
 
+@pytest.mark.parametrize("lens,n_q,Hq,Hk,d", [([3000], [20], 8, 8, 128), ([9000, 200], [40, 3], 4, 1, 64),
+                                              ([130, 1500, 0, 700], [17, 300, 2, 9], 8, 4, 128)])
+def test_few_rows_over_many_keys(lens, n_q, Hq, Hk, d):
+    """Too few row tiles for the GPU: their keys are cut into pieces, some of which see nothing of some rows."""
+    c = Case(lens, n_q, Hq, Hk, d, 32, seed=d, q_scale=2.0).poison_tails().device()
+    for causal, window in ((True, 0), (False, 0), (True, 257), (False, 64)):
+        c.check(causal=causal, window=window)
+
+
+def test_both_kernels_take_turns_on_one_workspace():
+    """Calls of few and of many rows, split over CTAs in either way, one after another with one workspace."""
+    c = Case([4000, 300], [30, 5], 8, 4, 128, 16, seed=21).device()
+    few = Case([4000, 300, 2000], [1, 1, 1], 8, 4, 128, 16, seed=22).device()
+    assert few.ws.numel() <= c.ws.numel()
+    few.ws = c.ws
+    first = c.run(0.09), few.run(0.09)
+    for _ in range(3):
+        c.check()
+        few.check()
+        for old, new in zip(first, (c.run(0.09), few.run(0.09))):
+            np.testing.assert_array_equal(old[0], new[0])
+            np.testing.assert_array_equal(old[1], new[1])
+
+
 @pytest.mark.parametrize("max_q,max_kv", [(1, 1), (1000, 10 ** 9), (0, 0), (7, 3000)])
 @pytest.mark.parametrize("n_q", [1, 90])
 def test_hints_do_not_change_the_result(max_q, max_kv, n_q):
