@@ -96,6 +96,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
+// a / b for a, b >= 0; 32-bit wherever that does (a 64-bit division is some 150 instructions).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // The line of units.  A request's tiles all run over its units [u_lo, u_hi).
 struct Walk {
   int b, tile, head, unit;  // the current unit
@@ -178,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
   // No piece is empty, so a tile's pieces are those of consecutive CTAs.
   const long long ctas = min((long long)gridDim.x, total);
   if (blockIdx.x >= ctas) return;
-  const long long u0 = blockIdx.x * total / ctas, u1 = (blockIdx.x + 1) * total / ctas;
+  const long long u0 = quotient(blockIdx.x * total, ctas), u1 = quotient((blockIdx.x + 1) * total, ctas);
   if (u0 >= before && u0 < before + mine) {  // exactly one thread
     long long rest = u0 - before;
     for (int b = rb0; b < rb1; ++b) {
@@ -187,10 +193,11 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
       const long long weight = walk_weight(p, w);
       if (rest < weight) {
         start_s[0] = b;
-        start_s[1] = (int)(rest / ((long long)p.kv_heads * w.n_units));
-        const long long in_tile = rest % ((long long)p.kv_heads * w.n_units);
-        start_s[2] = (int)(in_tile / w.n_units);
-        start_s[3] = (int)(in_tile % w.n_units);
+        const long long per_tile = (long long)p.kv_heads * w.n_units, tile = quotient(rest, per_tile);
+        const long long in_tile = rest - tile * per_tile, head = quotient(in_tile, w.n_units);
+        start_s[1] = (int)tile;
+        start_s[2] = (int)head;
+        start_s[3] = (int)(in_tile - head * w.n_units);
         break;
       }
       rest -= weight;
@@ -203,8 +210,7 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
   f.tile = start_s[1];
   f.head = start_s[2];
   f.unit = start_s[3];
-  int at_b = f.b, at_tile = f.tile, at_head = f.head, at_unit = f.unit;  // the unit to work on
-  long long n_left = u1 - u0, n_fetch = n_left;
+  int n_left = (int)(u1 - u0), n_fetch = n_left;  // (a piece has at most 2^36 / the CTAs)
   long long at = u0;  // the line's index of the current unit
 
   // --- fetching: this warp's 32 tokens of a unit into a stage ---------------------
@@ -220,39 +226,42 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
       if (tok < f.rq.hi && tok + 16 > f.rq.lo) next_page[h] = p.table[(int64_t)f.b * p.max_pages + (tok >> p.page_shift)];
     }
   };
+  // A lane's 16 bytes of eight rows of codes (d = 128; of sixteen at d = 64) lie at
+  // 16 * lane behind the first row.  K goes to the operands' row order, V's
+  // pieces are turned within a row so that reading them meets no bank twice.
+  constexpr int kCpr = D / 32;                             // 16-byte pieces of a row of codes
+  constexpr int kCopies = kWarpTokens * kCpr / 32;         // of K, and of V: 4 or 2
+  constexpr int kCopyRows = 32 / kCpr;
+  const int copy_row = lane / kCpr, copy_part = lane % kCpr;
+  const uint32_t k_dst = ((copy_row & ~7) | (2 * (copy_row & 3) + ((copy_row >> 2) & 1))) * (D / 2) + 16 * copy_part;
+  const uint32_t v_dst = St::kOffV + copy_row * (D / 2) + 16 * (D == 128 ? copy_part ^ (copy_row & 2) : copy_part);
+  // Scales: lanes 0 .. kScaleCopies - 1 K's, as many behind them V's.
+  constexpr int kScaleCopies = St::kScales / 16;
+  const bool scale_v = lane >= kScaleCopies, scale_second = (lane % kScaleCopies) >= kScaleCopies / 2;
+  const uint8_t* scale_src = (scale_v ? p.v_scales : p.k_scales) + 16 * (lane % (kScaleCopies / 2));
+  const uint32_t scale_dst = (scale_v ? St::kOffVs : St::kOffKs) + 16 * (lane % kScaleCopies);
+  const uint32_t page_tokens = (uint32_t)p.kv_heads << p.page_shift;  // at most 2^22
   auto fetch = [&](int stage) {
-    const int tok0 = (f.u_lo + f.unit) * kUnit + warp * kWarpTokens;
     const uint32_t base = ring + stage * St::kBytes;
-    const int ps = 1 << p.page_shift;
-    int64_t first[2];
+    const uint32_t tok0 = (f.u_lo + f.unit) * kUnit + warp * kWarpTokens, mask = (1u << p.page_shift) - 1;
     bool live[2];
+    uint64_t scale_at[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       live[h] = next_page[h] >= 0 && next_page[h] < p.num_pages;
-      first[h] = live[h] ? (((int64_t)next_page[h] * p.kv_heads + f.head) << p.page_shift) + ((tok0 + 16 * h) & (ps - 1)) : 0;
-    }
-    constexpr int kCpr = D / 32;                       // 16-byte chunks of a row of codes
-    constexpr int kCodeCopies = kWarpTokens * kCpr / 32;
+      const uint32_t page = live[h] ? next_page[h] : 0;
+      const uint32_t in_page = ((uint32_t)f.head << p.page_shift) + ((tok0 + 16 * h) & mask);
+      const uint64_t at = (uint64_t)page * (page_tokens * (D / 2)) + (in_page * (D / 2) + 16 * lane);
+      scale_at[h] = (uint64_t)page * (page_tokens * (D / 16)) + in_page * (D / 16);
 #pragma unroll
-    for (int i = 0; i < kCodeCopies; ++i) {
-      const int c = i * 32 + lane, row = c / kCpr, part = c % kCpr;
-      constexpr int kPerGroup = kCodeCopies / 2;
-      const int h = i / kPerGroup, x = row & 15;
-      const int64_t src = (first[h] + x) * (D / 2) + 16 * part;
-      const int krow = (row & ~7) | (2 * (x & 3) + ((x >> 2) & 1));  // the row of the K operand that holds token x
-      const int vpart = D == 128 ? part ^ (row & 2) : part;
-      copy16(base + krow * (D / 2) + 16 * part, p.k_codes + src, live[h]);
-      copy16(base + St::kOffV + row * (D / 2) + 16 * vpart, p.v_codes + src, live[h]);
+      for (int i = 0; i < kCopies / 2; ++i) {
+        const int k = h * (kCopies / 2) + i;
+        copy16(base + k_dst + k * (kCopyRows * D / 2), p.k_codes + at + i * 512, live[h]);
+        copy16(base + v_dst + k * (kCopyRows * D / 2), p.v_codes + at + i * 512, live[h]);
+      }
     }
-    constexpr int kScaleCopies = St::kScales / 16;     // 16 (d = 128) or 8, for each of K and V
-    if (lane < 2 * kScaleCopies) {
-      const bool is_v = lane >= kScaleCopies;
-      const int c = is_v ? lane - kScaleCopies : lane;
-      const bool second = c >= kScaleCopies / 2;
-      const uint8_t* src = (is_v ? p.v_scales : p.k_scales) + (second ? first[1] : first[0]) * (D / 16) +
-                           16 * (second ? c - kScaleCopies / 2 : c);
-      copy16(base + (is_v ? St::kOffVs : St::kOffKs) + 16 * c, src, second ? live[1] : live[0]);
-    }
+    if (lane < 2 * kScaleCopies)
+      copy16(base + scale_dst, scale_src + (scale_second ? scale_at[1] : scale_at[0]), scale_second ? live[1] : live[0]);
     return (live[0] ? 1 : 0) | (live[1] ? 2 : 0);
   };
   // Which groups of the stages in flight are there: two bits a stage.
@@ -270,43 +279,52 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
     asm volatile("cp.async.commit_group;" ::: "memory");
     fetch_stage = fetch_stage + 1 == kStages ? 0 : fetch_stage + 1;
   };
-  look_up();
+  // The query of a packed row (a division, where there are several).
+  auto query_of = [&](const Request& rq, uint32_t row) { return rq.n_q == 1 ? 0u : row / (uint32_t)p.group; };
+  // Query rows of a segment: this lane's quarter of row g of each n-tile.
+  uint4 raws[NT][D / 32];
+  auto load_query = [&]() {
+    const int n_rows = (int)min((int64_t)R, (int64_t)w.rq.n_q * p.group - (int64_t)w.tile * R);
 #pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) raws[nt][i] = make_uint4(0, 0, 0, 0);
+      if (r < n_rows) {
+        const uint32_t row = (uint32_t)w.tile * R + r, ti = query_of(w.rq, row), hd = row - ti * p.group;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(w.rq.row0 + ti) * p.ldq +
+                                                          (int64_t)(w.head * p.group + hd) * D + t * (D / 4));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) raws[nt][i] = src[i];
+      }
+    }
+  };
+  w = f;  // (before it is advanced any further)
+  look_up();
+  load_query();
+#pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) fetch_next();
   int stage = 0;
 
   bool first_segment = true;
   while (n_left > 0) {
     // --- a segment: consecutive units of one tile ---------------------------------
-    w.b = at_b;
-    load_walk(p, R, w);
-    const int seg_tile = at_tile, seg_head = at_head, seg_unit0 = at_unit, n_units = w.n_units;
+    const int seg_tile = w.tile, seg_head = w.head, seg_unit0 = w.unit, n_units = w.n_units;
     const Request rq = w.rq;
     const int seg_tok0 = (w.u_lo + seg_unit0) * kUnit + warp * kWarpTokens;
-    const int seg_n = (int)min(n_left, (long long)(n_units - seg_unit0));
+    const int seg_n = min(n_left, n_units - seg_unit0);
     const int n_rows = (int)min((int64_t)R, (int64_t)rq.n_q * p.group - (int64_t)seg_tile * R);
 
-    // Query rows: this lane's 32-th (d = 128) of row g of each n-tile, as FP16
-    // scaled by a power of two; and what the lane's accumulator columns need.
+    // The query as FP16, scaled by a power of two; and what the lane's accumulator
+    // columns need.
     uint32_t qf[NT][D / 8];
     float factor[NT][2];
     int lo_q[NT][2], hi_q[NT][2];
     int lo_max = 0, hi_min = rq.hi;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + g;
-      uint4 raw[D / 32];
+      const uint4(&raw)[D / 32] = raws[nt];
       uint32_t amax = 0;
-      if (r < n_rows) {
-        const uint32_t row = (uint32_t)seg_tile * R + r, ti = row / p.group, hd = row - ti * p.group;
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(rq.row0 + ti) * p.ldq +
-                                                          (int64_t)(seg_head * p.group + hd) * D + t * (D / 4));
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) raw[i] = src[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-      }
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -329,7 +347,7 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
         const int col = 2 * t + c, rr = nt * 8 + col;
         // Never 0: a hidden score of -inf stays -inf times it.
         factor[nt][c] = fmaxf(fabsf(p.qk_scale) * pow2(-__shfl_sync(0xFFFFFFFFu, e, 4 * col)), 1.17549435e-38f);
-        const int2 s = rr < n_rows ? seen_by(p, rq, (int)(((uint32_t)seg_tile * R + rr) / p.group)) : make_int2(0, rq.hi);
+        const int2 s = rr < n_rows ? seen_by(p, rq, (int)query_of(rq, (uint32_t)seg_tile * R + rr)) : make_int2(0, rq.hi);
         lo_q[nt][c] = s.x;
         hi_q[nt][c] = s.y;
         lo_max = max(lo_max, s.x);
@@ -548,6 +566,12 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 
+    // --- the next segment's query is on its way while this one is finished ------------
+    if (n_left > seg_n) {
+      w.unit += seg_n - 1;
+      advance(p, R, w);
+      load_query();
+    }
     // --- join the four warps -----------------------------------------------------------
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -574,7 +598,7 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
     const bool whole = seg_n == n_units;
     const int part = 2 * (int)blockIdx.x + (first_segment ? 0 : 1);
     auto store_row = [&](int row, int d, float4 o, float mm, float ll) {
-      const uint32_t rr = (uint32_t)seg_tile * R + row, ti = rr / p.group;
+      const uint32_t rr = (uint32_t)seg_tile * R + row, ti = query_of(rq, rr);
       const int64_t tok = rq.row0 + (int64_t)ti;
       const int head = seg_head * p.group + (int)(rr - ti * p.group);
       const float inv = ll > 0.0f ? p.v_gscale / ll : (ll == 0.0f ? 0.0f : ll);  // a NaN stays one
@@ -583,35 +607,41 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
       if (d == 0 && p.lse != nullptr)
         p.lse[tok * p.q_heads + head] = ll == 0.0f ? -INFINITY : (mm - kHead + log2f(ll)) * 0.6931471805599453f;
     };
-    for (int i = tid; i < n_rows * (D / 4); i += kThreads) {
-      const int row = i / (D / 4), d = 4 * (i % (D / 4));
-      float mm = -INFINITY;
+    // What the warps have left in o_s and ml_s, as one: emit(row, d, output, maximum, sum).
+    auto join_warps = [&](auto emit) {
+      for (int i = tid; i < n_rows * (D / 4); i += kThreads) {
+        const int row = i / (D / 4), d = 4 * (i % (D / 4));
+        float mm = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, ml_s[k * R + row].x);
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float ll = 0.0f;
+        for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, ml_s[k * R + row].x);
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float ll = 0.0f;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) {
-        const float2 ml = ml_s[k * R + row];
-        const float c = ml.x == mm ? 1.0f : exp2_fast(ml.x - mm);
-        const float4 x = *reinterpret_cast<const float4*>(o_s + (k * R + row) * Sm::kRowFloats + d);
-        o.x += c * x.x;
-        o.y += c * x.y;
-        o.z += c * x.z;
-        o.w += c * x.w;
-        ll += c * ml.y;
+        for (int k = 0; k < kWarps; ++k) {
+          const float2 ml = ml_s[k * R + row];
+          const float c = ml.x == mm ? 1.0f : exp2_fast(ml.x - mm);
+          const float4 x = *reinterpret_cast<const float4*>(o_s + (k * R + row) * Sm::kRowFloats + d);
+          o.x += c * x.x;
+          o.y += c * x.y;
+          o.z += c * x.z;
+          o.w += c * x.w;
+          ll += c * ml.y;
+        }
+        emit(row, d, o, mm, ll);
       }
-      if (whole) {
-        store_row(row, d, o, mm, ll);
-      } else {
+    };
+    if (whole) {
+      join_warps(store_row);
+    } else {
+      join_warps([&](int row, int d, float4 o, float mm, float ll) {
         *reinterpret_cast<float4*>(p.part_o + ((int64_t)part * R + row) * D + d) = o;
         if (d == 0) p.part_ml[(int64_t)part * R + row] = make_float2(mm, ll);
-      }
+      });
     }
     if (!whole) {
       // The pieces of this tile: CTA i has the line's units from i * total / ctas on.
       const long long a = at - seg_unit0, z = a + n_units - 1;
-      const int i0 = (int)(((a + 1) * ctas - 1) / total), i1 = (int)(((z + 1) * ctas - 1) / total);
+      const int i0 = (int)quotient((a + 1) * ctas - 1, total), i1 = (int)quotient((z + 1) * ctas - 1, total);
       __threadfence();
       __syncthreads();
       // A CTA is the first of at most one tile that goes on behind it, so the
@@ -620,25 +650,56 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
       __syncthreads();
       if (last_s) {
         __threadfence();
-        const int slot0 = 2 * i0 + ((long long)i0 * total / ctas == a ? 0 : 1);
-        for (int i = tid; i < n_rows * (D / 4); i += kThreads) {
+        const int slot0 = 2 * i0 + (quotient(i0 * total, ctas) == a ? 0 : 1);
+        // Few pieces: a thread an output.  Many: each warp joins every fourth piece of
+        // all outputs and leaves what it has where the warps' own results were.
+        const bool many = i1 - i0 >= 16;
+        const int by = many ? kWarps : 1;
+        for (int i = many ? lane : tid; i < n_rows * (D / 4); i += many ? 32 : kThreads) {
           const int row = i / (D / 4), d = 4 * (i % (D / 4));
           float mm = -INFINITY, ll = 0.0f;
           float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int c = i0; c <= i1; ++c) {
-            const int64_t slot = (int64_t)(c == i0 ? slot0 : 2 * c) * R + row;
-            const float2 ml = __ldcg(p.part_ml + slot);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot * D + d));
-            const float mn = fmaxf(mm, ml.x);
-            const float keep = mm == mn ? 1.0f : exp2_fast(mm - mn), add = ml.x == mn ? 1.0f : exp2_fast(ml.x - mn);
-            o.x = keep * o.x + add * x.x;
-            o.y = keep * o.y + add * x.y;
-            o.z = keep * o.z + add * x.z;
-            o.w = keep * o.w + add * x.w;
-            ll = keep * ll + add * ml.y;
+          for (int c0 = i0 + (many ? warp : 0); c0 <= i1; c0 += 8 * by) {  // eight pieces' loads at a time
+            float2 ml[8];
+            float4 x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int c = c0 + k * by;
+              ml[k] = make_float2(-INFINITY, 0.0f);
+              x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (c <= i1) {
+                const int64_t slot = (int64_t)(c == i0 ? slot0 : 2 * c) * R + row;
+                ml[k] = __ldcg(p.part_ml + slot);
+                x[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot * D + d));
+              }
+            }
+            float mn = mm;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mn = fmaxf(mn, ml[k].x);
+            const float keep = mm == mn ? 1.0f : exp2_fast(mm - mn);
+            o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+            ll *= keep;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float add = ml[k].x == mn ? 1.0f : exp2_fast(ml[k].x - mn);
+              o.x += add * x[k].x;
+              o.y += add * x[k].y;
+              o.z += add * x[k].z;
+              o.w += add * x[k].w;
+              ll += add * ml[k].y;
+            }
             mm = mn;
           }
-          store_row(row, d, o, mm, ll);
+          if (!many) {
+            store_row(row, d, o, mm, ll);
+          } else {
+            *reinterpret_cast<float4*>(o_s + (warp * R + row) * Sm::kRowFloats + d) = o;
+            if (d == 0) ml_s[warp * R + row] = make_float2(mm, ll);
+          }
+        }
+        if (many) {
+          __syncthreads();
+          join_warps(store_row);
         }
         if (tid == 0) p.count[i0] = 0;  // as the next call needs it
       }
@@ -646,11 +707,6 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
     first_segment = false;
     at += seg_n;
     n_left -= seg_n;
-    if (n_left > 0) {
-      w.b = at_b, w.tile = at_tile, w.head = at_head, w.unit = at_unit + seg_n - 1;
-      advance(p, R, w);
-      at_b = w.b, at_tile = w.tile, at_head = w.head, at_unit = w.unit;
-    }
     __syncthreads();  // o_s and ml_s are written again by the next segment
   }
 }
@@ -694,7 +750,10 @@ cudaError_t launch_kv_attn_split(const AttnParams& params, const KvAttnShape& sh
   // No more CTAs than there can be units.
   const int64_t tiles = (shape.total_q * p.group + 8 * nt - 1) / (8 * nt) + shape.batch;
   const int64_t per_tile = (shape.max_kv + kUnit - 1) / kUnit + 1;
-  const int64_t units = tiles * shape.kv_heads * per_tile;
+  int64_t units = tiles * shape.kv_heads * per_tile;
+  // Nor so many that joining a lone tile's pieces takes longer than they save.
+  const int64_t join = tiles * shape.kv_heads * 64;
+  if (units > join) units = join;
   if (shape.head_dim == 128)
     return nt == 1 ? launch_decode<128, 1>(p, units, s) : launch_decode<128, 2>(p, units, s);
   return nt == 1 ? launch_decode<64, 1>(p, units, s) : launch_decode<64, 2>(p, units, s);
