@@ -67,15 +67,20 @@ __device__ __forceinline__ int2 seen_by(const AttnParams& p, const Request& r, i
 // nothing else is ever kept there.
 constexpr int kCounters = 1024;
 
-// Up to this many rows (queries x heads of a group) a request go to the kernel for few rows.
-constexpr int64_t kFewRows = 16;
+// Up to this many rows (queries x heads of a group) in all, and up to this many a
+// request, always go to the kernel for few rows.
+constexpr int64_t kFewRows = 32;
 
-// Few rows a request (fh_kv_decode.cu).
+// Few rows a request (fh_kv_decode.cu), and tiles of many on the tcgen05 tensor
+// cores (fh_kv_prefill.cu).  The costs are estimates in microseconds, by which a
+// call's kernel is chosen; max_kv: cached tokens that a query may see, at most.
 size_t kv_attn_split_workspace(const KvAttnShape& s);
+double kv_attn_split_cost(const KvAttnShape& s, int64_t max_kv);
 cudaError_t launch_kv_attn_split(const kv::AttnParams& p, const KvAttnShape& shape, void* workspace, cudaStream_t s);
 
-// Tiles of many rows, on the tcgen05 tensor cores (fh_kv_prefill.cu).
 size_t kv_attn_tiles_workspace(const KvAttnShape& s);
-cudaError_t launch_kv_attn_tiles(const kv::AttnParams& p, const KvAttnShape& shape, void* workspace, cudaStream_t s);
+double kv_attn_tiles_cost(const KvAttnShape& s, int64_t max_kv);
+cudaError_t launch_kv_attn_tiles(const kv::AttnParams& p, const KvAttnShape& shape, int64_t max_kv, void* workspace,
+                                 cudaStream_t s);
 
 }  // namespace fh

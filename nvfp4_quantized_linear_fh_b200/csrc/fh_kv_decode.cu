@@ -7,7 +7,7 @@
 // HBM: at d = 128 a cached token of one KV head is 144 bytes, shared by the G
 // query heads of its group.
 //
-// Work split.  A tile is R = 8 NT query rows (row = token * G + head in group)
+// Work split.  A tile is eight query rows (row = token * G + head in group)
 // of one request and one KV head; its keys are cut into units of 128 tokens.
 // All units of all tiles form one line, which the CTAs cut into equal pieces,
 // so ragged requests load the GPU evenly.  A tile that lies within one CTA's
@@ -52,6 +52,7 @@ using namespace kv;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kTileRows = 8;                // query rows of a tile
 constexpr int kUnit = 128;                  // tokens of a unit
 constexpr int kWarpTokens = kUnit / kWarps; // 32
 constexpr int kStages = 3;
@@ -67,12 +68,12 @@ struct Stage {  // bytes of one warp's stage
   static constexpr int kOffKs = kCodes, kOffV = kCodes + kScales, kOffVs = 2 * kCodes + kScales;
 };
 
-template <int D, int NT>
+template <int D>
 struct Smem {
   static constexpr int kRing = kWarps * kStages * Stage<D>::kBytes;
   static constexpr int kRowFloats = D + 4;
-  static constexpr int kO = kWarps * 8 * NT * kRowFloats * 4;
-  static constexpr int kMl = kWarps * 8 * NT * 8;
+  static constexpr int kO = kWarps * kTileRows * kRowFloats * 4;
+  static constexpr int kMl = kWarps * kTileRows * 8;
   static constexpr int kBytes = kRing + kO + kMl;
 };
 
@@ -141,12 +142,12 @@ __device__ __forceinline__ void interleave(uint32_t x, uint32_t y, uint32_t& eve
   odd = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int R = 8 * NT;
+template <int D>
+__global__ void __launch_bounds__(kThreads, 3) kv_decode_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int R = kTileRows;
   constexpr int kMt = D / 16;            // 16-row tiles of the output's d
   using St = Stage<D>;
-  using Sm = Smem<D, NT>;
+  using Sm = Smem<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long scan_s[kWarps];
   __shared__ int start_s[4];
@@ -281,22 +282,18 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
   };
   // The query of a packed row (a division, where there are several).
   auto query_of = [&](const Request& rq, uint32_t row) { return rq.n_q == 1 ? 0u : row / (uint32_t)p.group; };
-  // Query rows of a segment: this lane's quarter of row g of each n-tile.
-  uint4 raws[NT][D / 32];
+  // Query rows of a segment: this lane's quarter of row g.
+  uint4 raws[D / 32];
   auto load_query = [&]() {
     const int n_rows = (int)min((int64_t)R, (int64_t)w.rq.n_q * p.group - (int64_t)w.tile * R);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + g;
+    for (int i = 0; i < D / 32; ++i) raws[i] = make_uint4(0, 0, 0, 0);
+    if (g < n_rows) {
+      const uint32_t row = (uint32_t)w.tile * R + g, ti = query_of(w.rq, row), hd = row - ti * p.group;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(w.rq.row0 + ti) * p.ldq +
+                                                        (int64_t)(w.head * p.group + hd) * D + t * (D / 4));
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) raws[nt][i] = make_uint4(0, 0, 0, 0);
-      if (r < n_rows) {
-        const uint32_t row = (uint32_t)w.tile * R + r, ti = query_of(w.rq, row), hd = row - ti * p.group;
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(w.rq.row0 + ti) * p.ldq +
-                                                          (int64_t)(w.head * p.group + hd) * D + t * (D / 4));
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) raws[nt][i] = src[i];
-      }
+      for (int i = 0; i < D / 32; ++i) raws[i] = src[i];
     }
   };
   w = f;  // (before it is advanced any further)
@@ -317,42 +314,38 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
 
     // The query as FP16, scaled by a power of two; and what the lane's accumulator
     // columns need.
-    uint32_t qf[NT][D / 8];
-    float factor[NT][2];
-    int lo_q[NT][2], hi_q[NT][2];
+    uint32_t qf[D / 8];
+    float factor[2];
+    int lo_q[2], hi_q[2];
     int lo_max = 0, hi_min = rq.hi;
+    uint32_t amax = 0;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const uint4(&raw)[D / 32] = raws[nt];
-      uint32_t amax = 0;
+    for (int i = 0; i < D / 32; ++i) {
+      const uint32_t v[4] = {raws[i].x, raws[i].y, raws[i].z, raws[i].w};
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      for (int k = 0; k < 4; ++k) amax = max(amax, max(v[k] & 0x7FFFu, (v[k] >> 16) & 0x7FFFu));
+    }
+    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+    const int e = query_exponent(amax);
+    // A negative scale goes to the query, so that larger scores are larger sums.
+    const float up = p.qk_scale < 0.0f ? -pow2(e) : pow2(e);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) amax = max(amax, max(v[k] & 0x7FFFu, (v[k] >> 16) & 0x7FFFu));
-      }
-      amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-      amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-      const int e = query_exponent(amax);
-      // A negative scale goes to the query, so that larger scores are larger sums.
-      const float up = p.qk_scale < 0.0f ? -pow2(e) : pow2(e);
+    for (int i = 0; i < D / 32; ++i) {
+      const uint32_t v[4] = {raws[i].x, raws[i].y, raws[i].z, raws[i].w};
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      for (int k = 0; k < 4; ++k) qf[4 * i + k] = pack_f16x2(bf16_lo(v[k]) * up, bf16_hi(v[k]) * up);
+    }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) qf[nt][4 * i + k] = pack_f16x2(bf16_lo(v[k]) * up, bf16_hi(v[k]) * up);
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = 2 * t + c, rr = nt * 8 + col;
-        // Never 0: a hidden score of -inf stays -inf times it.
-        factor[nt][c] = fmaxf(fabsf(p.qk_scale) * pow2(-__shfl_sync(0xFFFFFFFFu, e, 4 * col)), 1.17549435e-38f);
-        const int2 s = rr < n_rows ? seen_by(p, rq, (int)query_of(rq, (uint32_t)seg_tile * R + rr)) : make_int2(0, rq.hi);
-        lo_q[nt][c] = s.x;
-        hi_q[nt][c] = s.y;
-        lo_max = max(lo_max, s.x);
-        hi_min = min(hi_min, s.y);
-      }
+    for (int c = 0; c < 2; ++c) {
+      const int col = 2 * t + c;
+      // Never 0: a hidden score of -inf stays -inf times it.
+      factor[c] = fmaxf(fabsf(p.qk_scale) * pow2(-__shfl_sync(0xFFFFFFFFu, e, 4 * col)), 1.17549435e-38f);
+      const int2 s = col < n_rows ? seen_by(p, rq, (int)query_of(rq, (uint32_t)seg_tile * R + col)) : make_int2(0, rq.hi);
+      lo_q[c] = s.x;
+      hi_q[c] = s.y;
+      lo_max = max(lo_max, s.x);
+      hi_min = min(hi_min, s.y);
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
@@ -360,17 +353,14 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
       hi_min = min(hi_min, __shfl_xor_sync(0xFFFFFFFFu, hi_min, o));
     }
 
-    float acc[NT][kMt][4];
-    float m[NT][2], l[NT][2];
+    float acc[kMt][4];
+    float m[2], l[2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int i = 0; i < kMt; ++i)
 #pragma unroll
-      for (int i = 0; i < kMt; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.0f;
-      m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.0f;
-    }
+      for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.0f;
 
     for (int u = 0; u < seg_n; ++u) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
@@ -392,14 +382,12 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
           }
           __syncwarp();
         }
-        // --- scores: s[i][nt][c] for the tokens of the 16-row tile i -----------------
-        float s[2][NT][4];
+        // --- scores: s[i][c] for the tokens of the 16-row tile i -----------------
+        float s[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) s[i][nt][c] = 0.0f;
+          for (int c = 0; c < 4; ++c) s[i][c] = 0.0f;
           uint32_t ka[D / 32], kb[D / 32];  // rows g and g + 8: D / 4 nibbles each
           uint32_t sa, sb2;
           const int tok_g = (g >> 1) + 4 * (g & 1);  // the token that operand row g holds
@@ -426,13 +414,10 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
             const uint32_t xb = __byte_perm(hb, hb, (D == 128 && wd >= 2) ? 0x3232 : 0x1010);
             const uint32_t a0 = hmul2(e2m1x2_to_f16x2<0>(ka[wd]), xa), a2 = hmul2(e2m1x2_to_f16x2<1>(ka[wd]), xa);
             const uint32_t a1 = hmul2(e2m1x2_to_f16x2<0>(kb[wd]), xb), a3 = hmul2(e2m1x2_to_f16x2<1>(kb[wd]), xb);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_16816(s[i][nt], a0, a1, a2, a3, qf[nt][4 * wd], qf[nt][4 * wd + 1]);
+            mma_16816(s[i], a0, a1, a2, a3, qf[4 * wd], qf[4 * wd + 1]);
             const uint32_t c0 = hmul2(e2m1x2_to_f16x2<2>(ka[wd]), xa), c2 = hmul2(e2m1x2_to_f16x2<3>(ka[wd]), xa);
             const uint32_t c1 = hmul2(e2m1x2_to_f16x2<2>(kb[wd]), xb), c3 = hmul2(e2m1x2_to_f16x2<3>(kb[wd]), xb);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_16816(s[i][nt], c0, c1, c2, c3, qf[nt][4 * wd + 2], qf[nt][4 * wd + 3]);
+            mma_16816(s[i], c0, c1, c2, c3, qf[4 * wd + 2], qf[4 * wd + 3]);
           }
         }
         // --- scores of tokens not seen ---------------------------------------------------
@@ -442,60 +427,51 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
           for (int i = 0; i < 2; ++i) {
             const bool there = (lv >> i) & 1u;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const int tok = tok0 + 16 * i + 8 * (c >> 1) + tok_g;
-                if (!there || tok < lo_q[nt][c & 1] || tok >= hi_q[nt][c & 1]) s[i][nt][c] = -INFINITY;
-              }
+            for (int c = 0; c < 4; ++c) {
+              const int tok = tok0 + 16 * i + 8 * (c >> 1) + tok_g;
+              if (!there || tok < lo_q[c & 1] || tok >= hi_q[c & 1]) s[i][c] = -INFINITY;
+            }
           }
         }
         // --- running maximum: raised only when a score is well above it ------------------
         bool raise = false;
-        float top[NT][2];
+        float top[2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            // In log2 units (the factor is > 0).
-            top[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2])) * factor[nt][c];
-            raise = raise || top[nt][c] > m[nt][c] + kRaise;
-          }
+        for (int c = 0; c < 2; ++c) {
+          // In log2 units (the factor is > 0).
+          top[c] = fmaxf(fmaxf(s[0][c], s[0][c + 2]), fmaxf(s[1][c], s[1][c + 2])) * factor[c];
+          raise = raise || top[c] > m[c] + kRaise;
+        }
         if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int c = 0; c < 2; ++c) {
+            float v = top[c];
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+            const float mn = fmaxf(m[c], v);
+            const float keep = m[c] == mn ? 1.0f : exp2_fast(m[c] - mn);  // 0 from -inf
+            m[c] = mn;
+            l[c] *= keep;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float v = top[nt][c];
-              v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
-              v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
-              v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
-              const float mn = fmaxf(m[nt][c], v);
-              const float keep = m[nt][c] == mn ? 1.0f : exp2_fast(m[nt][c] - mn);  // 0 from -inf
-              m[nt][c] = mn;
-              l[nt][c] *= keep;
-#pragma unroll
-              for (int k = 0; k < kMt; ++k) {
-                acc[nt][k][c] *= keep;
-                acc[nt][k][c + 2] *= keep;
-              }
+            for (int k = 0; k < kMt; ++k) {
+              acc[k][c] *= keep;
+              acc[k][c + 2] *= keep;
             }
+          }
         }
         // --- P = 2^(s - m + 6), its sum, and its operand layout ----------------------------
-        uint32_t pb[2][NT][2];
+        uint32_t pb[2][2];
+        const float off0 = m[0] == -INFINITY ? 0.0f : kHead - m[0];
+        const float off1 = m[1] == -INFINITY ? 0.0f : kHead - m[1];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float off0 = m[nt][0] == -INFINITY ? 0.0f : kHead - m[nt][0];
-          const float off1 = m[nt][1] == -INFINITY ? 0.0f : kHead - m[nt][1];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float p0 = exp2_fast(fmaf(s[i][nt][0], factor[nt][0], off0)), p1 = exp2_fast(fmaf(s[i][nt][1], factor[nt][1], off1));
-            const float p2 = exp2_fast(fmaf(s[i][nt][2], factor[nt][0], off0)), p3 = exp2_fast(fmaf(s[i][nt][3], factor[nt][1], off1));
-            l[nt][0] += p0 + p2;
-            l[nt][1] += p1 + p3;
-            pb[i][nt][0] = transpose8x8(pack_f16x2(p0, p1));
-            pb[i][nt][1] = transpose8x8(pack_f16x2(p2, p3));
-          }
+        for (int i = 0; i < 2; ++i) {
+          const float p0 = exp2_fast(fmaf(s[i][0], factor[0], off0)), p1 = exp2_fast(fmaf(s[i][1], factor[1], off1));
+          const float p2 = exp2_fast(fmaf(s[i][2], factor[0], off0)), p3 = exp2_fast(fmaf(s[i][3], factor[1], off1));
+          l[0] += p0 + p2;
+          l[1] += p1 + p3;
+          pb[i][0] = transpose8x8(pack_f16x2(p0, p1));
+          pb[i][1] = transpose8x8(pack_f16x2(p2, p3));
         }
         // --- O^T += V^T P^T ------------------------------------------------------------------
 #pragma unroll
@@ -527,14 +503,13 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
             interleave(v[0][1], v[1][1], e1, o1);  // values 8..15
             interleave(v[2][0], v[3][0], e2, o2);  // tokens t + 8, t + 12
             interleave(v[2][1], v[3][1], e3, o3);
-            auto two = [&](uint32_t a, uint32_t b, uint32_t c, uint32_t d, int mt) {
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_16816(acc[nt][mt], a, b, c, d, pb[i][nt][0], pb[i][nt][1]);
+            auto out = [&](uint32_t a, uint32_t b, uint32_t c, uint32_t d, int mt) {
+              mma_16816(acc[mt], a, b, c, d, pb[i][0], pb[i][1]);
             };
 #define FH_KV_MT(byte)                                                                                              \
-  two(hmul2(e2m1x2_to_f16x2<byte>(e0), h01), hmul2(e2m1x2_to_f16x2<byte>(e1), h01),                                 \
+  out(hmul2(e2m1x2_to_f16x2<byte>(e0), h01), hmul2(e2m1x2_to_f16x2<byte>(e1), h01),                                 \
       hmul2(e2m1x2_to_f16x2<byte>(e2), h23), hmul2(e2m1x2_to_f16x2<byte>(e3), h23), 2 * byte);                      \
-  two(hmul2(e2m1x2_to_f16x2<byte>(o0), h01), hmul2(e2m1x2_to_f16x2<byte>(o1), h01),                                 \
+  out(hmul2(e2m1x2_to_f16x2<byte>(o0), h01), hmul2(e2m1x2_to_f16x2<byte>(o1), h01),                                 \
       hmul2(e2m1x2_to_f16x2<byte>(o2), h23), hmul2(e2m1x2_to_f16x2<byte>(o3), h23), 2 * byte + 1);
             FH_KV_MT(0)
             FH_KV_MT(1)
@@ -545,18 +520,17 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
             uint32_t e0, o0, e2, o2;
             interleave(v[0][0], v[1][0], e0, o0);
             interleave(v[2][0], v[3][0], e2, o2);
-            auto one = [&](uint32_t a, uint32_t b, uint32_t c, uint32_t d, int mt) {
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_16816(acc[nt][mt], a, b, c, d, pb[i][nt][0], pb[i][nt][1]);
+            auto out = [&](uint32_t a, uint32_t b, uint32_t c, uint32_t d, int mt) {
+              mma_16816(acc[mt], a, b, c, d, pb[i][0], pb[i][1]);
             };
             // Values 0..3 are bytes 0 and 1, values 4..7 bytes 2 and 3.
-            one(hmul2(e2m1x2_to_f16x2<0>(e0), h01), hmul2(e2m1x2_to_f16x2<2>(e0), h01),
+            out(hmul2(e2m1x2_to_f16x2<0>(e0), h01), hmul2(e2m1x2_to_f16x2<2>(e0), h01),
                 hmul2(e2m1x2_to_f16x2<0>(e2), h23), hmul2(e2m1x2_to_f16x2<2>(e2), h23), 0);
-            one(hmul2(e2m1x2_to_f16x2<0>(o0), h01), hmul2(e2m1x2_to_f16x2<2>(o0), h01),
+            out(hmul2(e2m1x2_to_f16x2<0>(o0), h01), hmul2(e2m1x2_to_f16x2<2>(o0), h01),
                 hmul2(e2m1x2_to_f16x2<0>(o2), h23), hmul2(e2m1x2_to_f16x2<2>(o2), h23), 1);
-            one(hmul2(e2m1x2_to_f16x2<1>(e0), h01), hmul2(e2m1x2_to_f16x2<3>(e0), h01),
+            out(hmul2(e2m1x2_to_f16x2<1>(e0), h01), hmul2(e2m1x2_to_f16x2<3>(e0), h01),
                 hmul2(e2m1x2_to_f16x2<1>(e2), h23), hmul2(e2m1x2_to_f16x2<3>(e2), h23), 2);
-            one(hmul2(e2m1x2_to_f16x2<1>(o0), h01), hmul2(e2m1x2_to_f16x2<3>(o0), h01),
+            out(hmul2(e2m1x2_to_f16x2<1>(o0), h01), hmul2(e2m1x2_to_f16x2<3>(o0), h01),
                 hmul2(e2m1x2_to_f16x2<1>(o2), h23), hmul2(e2m1x2_to_f16x2<3>(o2), h23), 3);
           }
         }
@@ -574,24 +548,21 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
     }
     // --- join the four warps -----------------------------------------------------------
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int c = 0; c < 2; ++c) {
+      float v = l[c];
+      v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+      v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+      v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+      const int row = 2 * t + c;
+      if (g == 0) ml_s[warp * R + row] = make_float2(m[c], v);
+      // The lane's d values are contiguous: D / 8 from g * D / 8.
+      float* dst = o_s + (warp * R + row) * Sm::kRowFloats + g * (D / 8);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float v = l[nt][c];
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
-        const int row = nt * 8 + 2 * t + c;
-        if (g == 0) ml_s[warp * R + row] = make_float2(m[nt][c], v);
-        // The lane's d values are contiguous: D / 8 from g * D / 8.
-        float* dst = o_s + (warp * R + row) * Sm::kRowFloats + g * (D / 8);
-#pragma unroll
-        for (int k = 0; k < kMt; k += 4) {
-          *reinterpret_cast<float4*>(dst + k) =
-              make_float4(acc[nt][k][c], acc[nt][k + 1][c], acc[nt][k + 2][c], acc[nt][k + 3][c]);
-          *reinterpret_cast<float4*>(dst + kMt + k) =
-              make_float4(acc[nt][k][c + 2], acc[nt][k + 1][c + 2], acc[nt][k + 2][c + 2], acc[nt][k + 3][c + 2]);
-        }
+      for (int k = 0; k < kMt; k += 4) {
+        *reinterpret_cast<float4*>(dst + k) =
+            make_float4(acc[k][c], acc[k + 1][c], acc[k + 2][c], acc[k + 3][c]);
+        *reinterpret_cast<float4*>(dst + kMt + k) =
+            make_float4(acc[k][c + 2], acc[k + 1][c + 2], acc[k + 2][c + 2], acc[k + 3][c + 2]);
       }
     }
     __syncthreads();
@@ -711,52 +682,58 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const __grid_consta
   }
 }
 
-template <int D, int NT>
-cudaError_t launch_decode(const AttnParams& p, int64_t units, cudaStream_t s) {
-  using Sm = Smem<D, NT>;
+template <int D>
+cudaError_t launch_decode(const AttnParams& p, int64_t ctas, cudaStream_t s) {
+  using Sm = Smem<D>;
   static DeviceTable resident;  // CTAs an SM holds
   int dev = 0;
   cudaGetDevice(&dev);
   const int per_sm = per_device(resident, dev, [](int) {
     cudaError_t e =
-        cudaFuncSetAttribute(kv_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kBytes);
+        cudaFuncSetAttribute(kv_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kBytes);
     int n = 0;
     if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv_decode_kernel<D, NT>, kThreads, Sm::kBytes);
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv_decode_kernel<D>, kThreads, Sm::kBytes);
     return e != cudaSuccess ? -(int)e : (n < 1 ? 1 : n);
   });
   if (per_sm <= 0) return (cudaError_t)(-per_sm);
   int64_t grid = (int64_t)sm_count() * per_sm;
   if (grid > kMaxCtas) grid = kMaxCtas;
-  if (grid > units) grid = units;
-  kv_decode_kernel<D, NT><<<(int)grid, kThreads, Sm::kBytes, s>>>(p);
+  if (grid > ctas) grid = ctas;
+  kv_decode_kernel<D><<<(int)grid, kThreads, Sm::kBytes, s>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t kv_attn_split_workspace(const KvAttnShape& s) {
-  // count, then two partial tiles of at most 16 rows per CTA.
-  return kMaxCtas * sizeof(unsigned) + (size_t)2 * kMaxCtas * 16 * (size_t)(s.head_dim + 2) * sizeof(float);
+  // The counters, then two partial tiles per CTA.
+  return kMaxCtas * sizeof(unsigned) + (size_t)2 * kMaxCtas * kTileRows * (size_t)(s.head_dim + 2) * sizeof(float);
+}
+
+// Tiles of all KV heads, at most.
+int64_t split_tiles(const KvAttnShape& s) {
+  const int64_t rows = s.total_q * (s.q_heads / s.kv_heads), most = rows < s.batch ? rows : s.batch;
+  return (rows / kTileRows + most) * s.kv_heads;
+}
+
+double kv_attn_split_cost(const KvAttnShape& s, int64_t max_kv) {
+  // Every 32 tokens of a tile take about 0.8 ns (0.5 at d = 64) on the whole GPU,
+  // a tile 5 ns beside, and many requests of up to max_kv tokens have fewer.
+  const double part = s.batch >= 8 ? 0.6 : 1.0, tiles = (double)split_tiles(s);
+  return 9.0 + tiles * (0.005 + (s.head_dim == 64 ? 0.0005 : 0.0008) * part * (double)max_kv / kWarpTokens);
 }
 
 cudaError_t launch_kv_attn_split(const AttnParams& params, const KvAttnShape& shape, void* workspace, cudaStream_t s) {
   AttnParams p = params;
   p.count = static_cast<unsigned*>(workspace);
   p.part_o = reinterpret_cast<float*>(p.count + kMaxCtas);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)2 * kMaxCtas * 16 * shape.head_dim);
-  const int64_t rows = shape.max_q * p.group;
-  const int nt = rows <= 8 ? 1 : 2;
-  // No more CTAs than there can be units.
-  const int64_t tiles = (shape.total_q * p.group + 8 * nt - 1) / (8 * nt) + shape.batch;
-  const int64_t per_tile = (shape.max_kv + kUnit - 1) / kUnit + 1;
-  int64_t units = tiles * shape.kv_heads * per_tile;
-  // Nor so many that joining a lone tile's pieces takes longer than they save.
-  const int64_t join = tiles * shape.kv_heads * 64;
-  if (units > join) units = join;
-  if (shape.head_dim == 128)
-    return nt == 1 ? launch_decode<128, 1>(p, units, s) : launch_decode<128, 2>(p, units, s);
-  return nt == 1 ? launch_decode<64, 1>(p, units, s) : launch_decode<64, 2>(p, units, s);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)2 * kMaxCtas * kTileRows * shape.head_dim);
+  // No more CTAs than there can be units; nor so many that joining a lone tile's
+  // pieces takes longer than they save.
+  const int64_t tiles = split_tiles(shape), per_tile = (shape.max_kv + kUnit - 1) / kUnit + 1;
+  const int64_t ctas = tiles * (per_tile < 64 ? per_tile : 64);
+  return shape.head_dim == 128 ? launch_decode<128>(p, ctas, s) : launch_decode<64>(p, ctas, s);
 }
 
 }  // namespace fh

@@ -819,17 +819,16 @@ int64_t most_units(const KvAttnShape& shape) {
 
 // Into how many pieces the keys of a row tile are cut: as many as shorten the
 // call, a CTA taking about as long as three key tiles to start and finish and
-// the join of pieces as long as two more.
-int pieces_for(int64_t units, int64_t max_kv, int window, int sms) {
-  if (units >= sms) return 1;
-  if (window > 0 && max_kv > (int64_t)window + kRows * kTiles) max_kv = (int64_t)window + kRows * kTiles;
-  const int64_t keys = (max_kv + kKeys - 1) / kKeys;
+// the join of pieces as long as two more.  *cost: key tiles in a row.
+int pieces_for(int64_t units, int64_t max_kv, int sms, double* cost) {
+  const double keys = (double)((max_kv + kKeys - 1) / kKeys);
   int best = 1;
-  int64_t best_cost = keys + 3;
-  for (int n = 2; n <= kMaxPieces && units * n <= kMaxPieceCtas; ++n) {
-    const int64_t cost = (units * n + sms - 1) / sms * ((keys + n - 1) / n + 3) + 2;
-    if (cost < best_cost) {
-      best_cost = cost;
+  // Many row tiles end at different times, so that a last wave costs its share only.
+  *cost = (units > sms ? (double)units / sms : 1.0) * (keys + 3);
+  for (int n = 2; n <= kMaxPieces && units < sms && units * n <= kMaxPieceCtas; ++n) {
+    const double c = (double)((units * n + sms - 1) / sms) * (ceil(keys / n) + 3) + 2;
+    if (c < *cost) {
+      *cost = c;
       best = n;
     }
   }
@@ -845,10 +844,18 @@ size_t kv_attn_tiles_workspace(const KvAttnShape& s) {
   return kCounters * sizeof(unsigned) + (size_t)ctas * (kRows * kTiles) * (size_t)(s.head_dim + 2) * sizeof(float);
 }
 
-cudaError_t launch_kv_attn_tiles(const AttnParams& params, const KvAttnShape& shape, void* workspace, cudaStream_t s) {
+double kv_attn_tiles_cost(const KvAttnShape& s, int64_t max_kv) {
+  double cost;
+  pieces_for(most_units(s), max_kv, sm_count(), &cost);
+  return 7.0 + 1.8 * (s.batch >= 8 ? 0.85 : 1.0) * cost;  // 1.8 us a key tile, whatever d and the rows of the last tile
+}
+
+cudaError_t launch_kv_attn_tiles(const AttnParams& params, const KvAttnShape& shape, int64_t max_kv, void* workspace,
+                                 cudaStream_t s) {
   AttnParams p = params;
   const int64_t units = most_units(shape);
-  const int pieces = pieces_for(units, shape.max_kv, p.window, sm_count());
+  double cost;
+  const int pieces = pieces_for(units, max_kv, sm_count(), &cost);
   p.count = static_cast<unsigned*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.count + kCounters);
   p.part_o = reinterpret_cast<float*>(p.part_ml + units * pieces * (kRows * kTiles));
