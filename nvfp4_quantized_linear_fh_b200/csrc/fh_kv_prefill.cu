@@ -80,7 +80,7 @@ struct Cfg {
   static constexpr int kRawBytes = kRawCodes + kRawScales;
   static constexpr int kOffRaw = kOffV + kStages * kOperand;
   static constexpr int kOffBar = kOffRaw + kRaw * kRawBytes;
-  static constexpr int kBars = 4 * kStages + 4 * kTiles + 2 + 2 * kRaw;
+  static constexpr int kBars = 2 * kStages + 4 * kTiles + 4 + 2 * kRaw;
   static constexpr int kOffLive = kOffBar + 8 * kBars;
   static constexpr int kOffRawLive = kOffLive + 8 * kLive;
   static constexpr int kOffMisc = kOffRawLive + 8 * kRaw;
@@ -188,6 +188,11 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lead) {
   return dsc;
 }
 
+// A descriptor `bytes` on: the address is in the low word, and stays there.
+__device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) {
+  return (d & 0xFFFFFFFF00000000ull) | (uint32_t)((uint32_t)d + (bytes >> 4));
+}
+
 // tcgen05.mma kind::f16: FP16 operands, FP32 accumulator; M = 128.
 __host__ __device__ constexpr uint32_t idesc(int n, bool b_mn_major) {
   return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
@@ -275,15 +280,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = s_u32(smem);
   const uint32_t bar0 = sbase + C::kOffBar;
-  auto kfull = [&](int s) { return bar0 + 8u * s; };
-  auto kempty = [&](int s) { return bar0 + 8u * (kStages + s); };
-  auto vfull = [&](int s) { return bar0 + 8u * (2 * kStages + s); };
-  auto vempty = [&](int s) { return bar0 + 8u * (3 * kStages + s); };
-  auto sfull = [&](int t) { return bar0 + 8u * (4 * kStages + t); };            // scores written
-  auto pfull = [&](int t, int half) { return bar0 + 8u * (4 * kStages + kTiles + 2 * t + half); };  // P of 64 keys written
-  auto ofull = [&](int t) { return bar0 + 8u * (4 * kStages + 3 * kTiles + t); };
-  const uint32_t qfull = bar0 + 8u * (4 * kStages + 4 * kTiles);
-  const uint32_t drained = qfull + 8u;
+  auto kempty = [&](int s) { return bar0 + 8u * s; };
+  auto vempty = [&](int s) { return bar0 + 8u * (kStages + s); };
+  const uint32_t bar1 = bar0 + 16u * kStages;
+  auto sfull = [&](int t) { return bar1 + 8u * t; };                  // scores written
+  auto pfull = [&](int t, int half) { return bar1 + 8u * (kTiles + 2 * t + half); };  // P of 64 keys written
+  auto ofull = [&](int t) { return bar1 + 8u * (3 * kTiles + t); };
+  // Tile 0's first half of P(j) waits for V(j) and K(j + 1) as well: a wait less
+  // for the product thread.  K may be there two steps ahead, so that odd steps
+  // have a barrier of their own.
+  const uint32_t pfirst_odd = bar1 + 8u * (4 * kTiles);
+  auto pfirst = [&](int j) { return (j & 1) ? pfirst_odd : pfull(0, 0); };
+  const uint32_t qfull = pfirst_odd + 8u, k0full = qfull + 8u, drained = qfull + 16u;
   auto rfull = [&](int i) { return drained + 8u + 8u * i; };
   auto rempty = [&](int i) { return drained + 8u + 8u * (kRaw + i); };
   uint64_t* live_s = reinterpret_cast<uint64_t*>(smem + C::kOffLive);     // a byte per 16 keys: their page is there
@@ -335,18 +343,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      bar_init(kfull(s), kFeedWarps);
       bar_init(kempty(s), 1);
-      bar_init(vfull(s), kFeedWarps);
       bar_init(vempty(s), 1);
     }
     for (int t = 0; t < kTiles; ++t) {
       bar_init(sfull(t), 1);
-      bar_init(pfull(t, 0), 4);
+      bar_init(pfull(t, 0), t == 0 ? 4 + kFeedWarps : 4);
       bar_init(pfull(t, 1), 4);
       bar_init(ofull(t), 1);
     }
+    bar_init(pfirst_odd, 4 + kFeedWarps);
     bar_init(qfull, kSoftWarps);
+    bar_init(k0full, kFeedWarps);
     bar_init(drained, 1);
     for (int i = 0; i < kRaw; ++i) {
       bar_init(rfull(i), 1);
@@ -513,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (c & 1) {  // 64 keys' P: the product may start on them
             tmem_stored();
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            warp_arrive(pfull(t, c >> 1), lane);
+            warp_arrive(t == 0 && c == 1 ? pfirst(j) : pfull(t, c >> 1), lane);
           }
         }
       }
@@ -670,7 +678,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kPieces; ++i) put(dst, row_in + i * (128 / kCpr), codes[i], scales[i]);
       if (!is_v && x == 0) live_s[j % kLive] = live;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      warp_arrive(is_v ? vfull(s) : kfull(s), lane);
+      if (!is_v)
+        warp_arrive(j == 0 ? k0full : pfirst(j - 1), lane);  // V(j - 1) is there, too
+      else if (j + 1 == job.n_keys)
+        warp_arrive(pfirst(j), lane);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -681,19 +692,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t b = sw128_desc(sbase + C::kOffK + s * C::kOperand, 16);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const uint64_t step = (uint64_t)(((k >> 2) * C::kHalfBytes + (k & 3) * 32) >> 4);
-        mma_ss(tmem + C::kTmemS + t * kKeys, a + step, b + step, idesc(kKeys, false), k > 0);
+        const uint32_t step = (k >> 2) * C::kHalfBytes + (k & 3) * 32;
+        mma_ss(tmem + C::kTmemS + t * kKeys, desc_add(a, step), desc_add(b, step), idesc(kKeys, false), k > 0);
       }
     };
     auto output = [&](int t, int s, int half, bool accumulate) {  // O_t += P_t V over 64 keys
       const uint64_t b = sw128_desc(sbase + C::kOffV + s * C::kOperand, C::kHalfBytes);
 #pragma unroll
       for (int k = 4 * half; k < 4 * half + 4; ++k)
-        mma_ts(tmem + C::kTmemO + t * D, tmem + C::kTmemS + t * kKeys + 8 * k, b + (uint64_t)(k * 2048 >> 4),
+        mma_ts(tmem + C::kTmemO + t * D, tmem + C::kTmemS + t * kKeys + 8 * k, desc_add(b, k * 2048),
                idesc(D, true), accumulate || k > 0);
     };
     if (elect()) {  // one thread waits and issues: no votes between a wait and its product
-      bool ok = job.n_keys > 0 && bar_wait(qfull, 0, abort_flag) && bar_wait(kfull(0), 0, abort_flag);
+      bool ok = job.n_keys > 0 && bar_wait(qfull, 0, abort_flag) && bar_wait(k0full, 0, abort_flag);
       if (ok) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         for (int t = 0; t < tiles; ++t) {
@@ -705,10 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < job.n_keys && ok; ++j) {
         const int s = j % kStages, sn = (j + 1) % kStages;
         const bool more = j + 1 < job.n_keys;
-        ok = bar_wait(vfull(s), (j / kStages) & 1, abort_flag) &&
-             (!more || bar_wait(kfull(sn), ((j + 1) / kStages) & 1, abort_flag));
         for (int t = 0; t < tiles && ok; ++t) {
-          ok = bar_wait(pfull(t, 0), j & 1, abort_flag);
+          ok = t == 0 ? bar_wait(pfirst(j), (j >> 1) & 1, abort_flag) : bar_wait(pfull(t, 0), j & 1, abort_flag);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           output(t, s, 0, j > 0);
