@@ -2,8 +2,10 @@
 // request (prompts, whole clips), on the tcgen05 tensor cores.
 //
 // The same attention as fh_kv_decode.cu; here the two products bound it, and
-// beside them the exponentials: 256 rows x 128 keys take 2048 cycles of a
-// SM's FP16 tensor rate at d = 128, and as many of its 16 exponentials a cycle.
+// beside them the exponentials.  At d = 128, 256 rows x 128 keys are 2048
+// cycles of an SM's nominal FP16 tensor rate; as issued, 2868 (measured alone:
+// a 128 x 128 x 16 MMA takes 105 cycles with A in shared memory, 74 with A in
+// TMEM), and 2048 of its 16 exponentials a cycle.
 //
 // A CTA has 256 packed query rows (row = token * G + head in group) of one
 // request and KV head, as two 128-row tiles, and walks 128-token key tiles:
@@ -26,10 +28,11 @@
 // more than 8 (in log2), by the row's own thread: the commit that announces
 // S(j) also covers O += P(j-1) V, so nothing else is writing O then.
 //
-// Few rows over many keys (too few tiles for the GPU): the key tiles of a row
-// tile are cut into up to eight pieces, a CTA each, which leave their partial
-// results in the workspace; the one that finishes last (an atomic count; nobody
-// waits) joins them in the pieces' order.
+// Too few row tiles for the GPU, or too few in its last wave: their keys are cut
+// into up to eight pieces, a CTA each, which leave their partial results in the
+// workspace; the one that finishes last (an atomic count; nobody waits) joins
+// them in the pieces' order.  (At 21 x 4096 x 4096 x 128, 336 tiles on 148 SMs,
+// the last 40 as 120 thirds.)
 //
 // Queries, probabilities, sums and roundings are as in fh_kv_decode.cu.  Every
 // mbarrier wait is bounded; on expiry the kernel sets its error word, drains
@@ -274,7 +277,7 @@ struct Job {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    kv_prefill_kernel(const __grid_constant__ AttnParams p, int pieces) {
+    kv_prefill_kernel(const __grid_constant__ AttnParams p, int whole, int cut) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -326,7 +329,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (i < warp) before += scan_s[i];
     total += scan_s[i];
   }
-  const int unit = (int)blockIdx.x / pieces, piece = (int)blockIdx.x % pieces;  // a row tile of a KV head, and which keys
+  // The first `whole` CTAs have a row tile of a KV head each, the others a piece
+  // of one cut into `cut`.
+  const int part_id = (int)blockIdx.x - whole;  // place of the partial result
+  const int pieces = part_id < 0 ? 1 : cut, piece = part_id < 0 ? 0 : part_id % cut;
+  const int cut_unit = part_id < 0 ? 0 : part_id / cut;
+  const int unit = part_id < 0 ? (int)blockIdx.x : whole + cut_unit;
   const int slot = total - 1 - unit / p.kv_heads;
   if (slot < 0) return;
   if (slot >= before && slot < before + mine) {
@@ -531,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float weight[kMaxPieces];  // of the pieces' partial outputs
       if (pieces > 1) {  // (also when a wait has run out: all of these warps meet at the barriers)
         // Partial results, column by column: a warp's 32 rows lie together.
-        float* part = p.part_o + (int64_t)blockIdx.x * (kCtaRows * D) + row;
+        float* part = p.part_o + (int64_t)part_id * (kCtaRows * D) + row;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
@@ -545,18 +553,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) part[(32 * c + i) * kCtaRows] = __uint_as_float(v[i]);
         }
-        p.part_ml[(int64_t)blockIdx.x * kCtaRows + row] = make_float2(m, l);
+        p.part_ml[(int64_t)part_id * kCtaRows + row] = make_float2(m, l);
         __threadfence();
         asm volatile("bar.sync 1, %0;" ::"r"(kRows * tiles) : "memory");  // the softmax warps that have rows
         if (tid == 0) {
-          last_s = atomicAdd(p.count + unit, 1u) == (unsigned)(pieces - 1);
-          if (last_s) p.count[unit] = 0;  // as the next call needs it
+          last_s = atomicAdd(p.count + cut_unit, 1u) == (unsigned)(pieces - 1);
+          if (last_s) p.count[cut_unit] = 0;  // as the next call needs it
         }
         asm volatile("bar.sync 1, %0;" ::"r"(kRows * tiles) : "memory");
         ok = ok && last_s != 0;  // the others are done
         if (ok) {
           __threadfence();
-          const float2* ml = p.part_ml + (int64_t)unit * pieces * kCtaRows + row;
+          const float2* ml = p.part_ml + (int64_t)cut_unit * pieces * kCtaRows + row;
           float ms[kMaxPieces], ls[kMaxPieces];
           m = -INFINITY;
 #pragma unroll
@@ -583,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
           if (pieces > 1) {
-            const float* part = p.part_o + (int64_t)unit * pieces * (kCtaRows * D) + (32 * c) * kCtaRows + row;
+            const float* part = p.part_o + (int64_t)cut_unit * pieces * (kCtaRows * D) + (32 * c) * kCtaRows + row;
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0;
 #pragma unroll 1
@@ -805,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-cudaError_t launch_prefill(const AttnParams& p, int64_t units, int pieces, cudaStream_t s) {
+cudaError_t launch_prefill(const AttnParams& p, int64_t whole, int64_t rest, int cut, cudaStream_t s) {
   using C = Cfg<D>;
   static DeviceTable configured;
   int dev = 0;
@@ -816,59 +824,72 @@ cudaError_t launch_prefill(const AttnParams& p, int64_t units, int pieces, cudaS
     return e == cudaSuccess ? 1 : -(int)e;
   });
   if (cfg <= 0) return (cudaError_t)(-cfg);
-  kv_prefill_kernel<D><<<(unsigned)(units * pieces), kThreads, C::kSmem, s>>>(p, pieces);
+  kv_prefill_kernel<D><<<(unsigned)(whole + rest * cut), kThreads, C::kSmem, s>>>(p, (int)whole, cut);
   return cudaGetLastError();
 }
 
 // As many row tiles (of all KV heads) as there can be: a request's last one may be short.
 int64_t most_units(const KvAttnShape& shape) {
+  constexpr int64_t kCtaRows = kRows * kTiles;
   const int64_t rows = shape.total_q * (shape.q_heads / shape.kv_heads), most = rows < shape.batch ? rows : shape.batch;
-  return (rows / (kRows * kTiles) + most) * shape.kv_heads;
+  return (rows + (kCtaRows - 1) * most) / kCtaRows * shape.kv_heads;
 }
 
-// Into how many pieces the keys of a row tile are cut: as many as shorten the
-// call, a CTA taking about as long as three key tiles to start and finish and
-// the join of pieces as long as two more.  *cost: key tiles in a row.
-int pieces_for(int64_t units, int64_t max_kv, int sms, double* cost) {
+// How a call's row tiles go to CTAs: `whole` of them as they are, the `rest`
+// that would be an unfilled wave cut into `cut` pieces each.
+struct Plan {
+  int64_t whole, rest;
+  int cut;
+  double cost;  // in key tiles, one after another
+};
+
+// As many pieces as shorten the call, a CTA taking about as long as three key
+// tiles to start and finish, and the join of pieces as long as two.
+Plan plan_for(int64_t units, int64_t max_kv, int sms) {
   const double keys = (double)((max_kv + kKeys - 1) / kKeys);
-  int best = 1;
-  // Many row tiles end at different times, so that a last wave costs its share only.
-  *cost = (units > sms ? (double)units / sms : 1.0) * (keys + 3);
-  for (int n = 2; n <= kMaxPieces && units < sms && units * n <= kMaxPieceCtas; ++n) {
-    const double c = (double)((units * n + sms - 1) / sms) * (ceil(keys / n) + 3) + 2;
-    if (c < *cost) {
-      *cost = c;
-      best = n;
+  Plan plan;
+  plan.whole = units / sms * sms;
+  plan.rest = units - plan.whole;
+  plan.cut = 1;
+  double best = plan.rest > 0 ? keys + 3 : 0.0;
+  for (int n = 2; n <= kMaxPieces && plan.rest * n <= kMaxPieceCtas; ++n) {
+    const double c = (double)((plan.rest * n + sms - 1) / sms) * (ceil(keys / n) + 3) + 2;
+    if (c < best) {
+      best = c;
+      plan.cut = n;
     }
   }
-  return best;
+  if (plan.cut == 1) {
+    plan.whole += plan.rest;
+    plan.rest = 0;
+  }
+  plan.cost = (double)(units / sms) * (keys + 3) + best;
+  return plan;
 }
 
 }  // namespace
 
 size_t kv_attn_tiles_workspace(const KvAttnShape& s) {
-  const int64_t units = most_units(s), ctas = units * kMaxPieces < kMaxPieceCtas ? units * kMaxPieces : kMaxPieceCtas;
   if (s.total_q * (s.q_heads / s.kv_heads) <= kFewRows) return 0;  // never comes here
-  // (No less for more units, of which none is cut: a workspace serves smaller calls too.)
+  // (No less for more units, of which fewer may be cut: a workspace serves smaller calls too.)
+  const int64_t units = most_units(s), ctas = units * kMaxPieces < kMaxPieceCtas ? units * kMaxPieces : kMaxPieceCtas;
   return kCounters * sizeof(unsigned) + (size_t)ctas * (kRows * kTiles) * (size_t)(s.head_dim + 2) * sizeof(float);
 }
 
 double kv_attn_tiles_cost(const KvAttnShape& s, int64_t max_kv) {
-  double cost;
-  pieces_for(most_units(s), max_kv, sm_count(), &cost);
-  return 7.0 + 1.8 * (s.batch >= 8 ? 0.85 : 1.0) * cost;  // 1.8 us a key tile, whatever d and the rows of the last tile
+  // 1.8 us a key tile, whatever d and the rows of the last tile; tiles of many requests end at different times.
+  return 7.0 + 1.8 * (s.batch >= 8 ? 0.85 : 1.0) * plan_for(most_units(s), max_kv, sm_count()).cost;
 }
 
 cudaError_t launch_kv_attn_tiles(const AttnParams& params, const KvAttnShape& shape, int64_t max_kv, void* workspace,
                                  cudaStream_t s) {
   AttnParams p = params;
-  const int64_t units = most_units(shape);
-  double cost;
-  const int pieces = pieces_for(units, max_kv, sm_count(), &cost);
+  const Plan plan = plan_for(most_units(shape), max_kv, sm_count());
   p.count = static_cast<unsigned*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.count + kCounters);
-  p.part_o = reinterpret_cast<float*>(p.part_ml + units * pieces * (kRows * kTiles));
-  return shape.head_dim == 128 ? launch_prefill<128>(p, units, pieces, s) : launch_prefill<64>(p, units, pieces, s);
+  p.part_o = reinterpret_cast<float*>(p.part_ml + plan.rest * plan.cut * (kRows * kTiles));
+  return shape.head_dim == 128 ? launch_prefill<128>(p, plan.whole, plan.rest, plan.cut, s)
+                               : launch_prefill<64>(p, plan.whole, plan.rest, plan.cut, s);
 }
 
 cudaError_t read_and_clear_kv_error(unsigned int* bits) {
