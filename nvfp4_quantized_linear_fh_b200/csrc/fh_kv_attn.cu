@@ -31,7 +31,7 @@ cudaError_t launch_kv_attention(const fh_kv_cache& c, const KvAttnCall& call, co
   p.batch = (int)shape.batch;
   p.q_heads = (int)shape.q_heads;
   p.kv_heads = (int)shape.kv_heads;
-  p.group = (int)(shape.q_heads / shape.kv_heads);
+  kv::set_group(&p, (int)(shape.q_heads / shape.kv_heads));
   p.page_shift = 0;
   while (((int64_t)1 << p.page_shift) < c.page_size) ++p.page_shift;
   p.num_pages = (int)c.num_pages;

@@ -22,6 +22,8 @@ struct AttnParams {
   const int32_t* q_starts;  // [batch + 1]
   int64_t ldq, ldo, max_pages;
   int total_q, batch, q_heads, kv_heads, group;  // group = q_heads / kv_heads
+  uint32_t group_magic;  // of the division by it, with group_shift (set_group)
+  int group_shift;
   int page_shift, num_pages;
   int causal, window;
   float qk_scale;  // sm_scale * log2(e) * k_gscale: scores in units of log2
@@ -31,6 +33,21 @@ struct AttnParams {
   float2* part_ml;      // [slots][rows]: running maximum (log2 units) and sum
   unsigned int* count;  // zero between calls
 };
+
+// row / group for 0 <= row < 2^31: with s = ceil(log2 group) and m =
+// floor(2^(31 + s) / group) + 1, m group exceeds 2^(31 + s) by at most 2^s, so
+// that row m / 2^(31 + s) is above row / group by less than 1 / group.
+inline void set_group(AttnParams* p, int group) {
+  int s = 0;
+  while (((int64_t)1 << s) < group) ++s;
+  p->group = group;
+  p->group_shift = s - 1;
+  p->group_magic = group == 1 ? 0u : (uint32_t)(((uint64_t)1 << (31 + s)) / (uint64_t)group + 1);
+}
+
+__device__ __forceinline__ uint32_t query_of_row(const AttnParams& p, uint32_t row) {
+  return p.group == 1 ? row : __umulhi(row, p.group_magic) >> p.group_shift;
+}
 
 // One request as every kernel reads it, with the lengths brought into range so
 // that no index built from them leaves a buffer.

@@ -280,8 +280,6 @@ __global__ void __launch_bounds__(kThreads, 3) kv_decode_kernel(const __grid_con
     asm volatile("cp.async.commit_group;" ::: "memory");
     fetch_stage = fetch_stage + 1 == kStages ? 0 : fetch_stage + 1;
   };
-  // The query of a packed row (a division, where there are several).
-  auto query_of = [&](const Request& rq, uint32_t row) { return rq.n_q == 1 ? 0u : row / (uint32_t)p.group; };
   // Query rows of a segment: this lane's quarter of row g.
   uint4 raws[D / 32];
   auto load_query = [&]() {
@@ -289,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_decode_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) raws[i] = make_uint4(0, 0, 0, 0);
     if (g < n_rows) {
-      const uint32_t row = (uint32_t)w.tile * R + g, ti = query_of(w.rq, row), hd = row - ti * p.group;
+      const uint32_t row = (uint32_t)w.tile * R + g, ti = query_of_row(p, row), hd = row - ti * p.group;
       const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(w.rq.row0 + ti) * p.ldq +
                                                         (int64_t)(w.head * p.group + hd) * D + t * (D / 4));
 #pragma unroll
@@ -341,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_decode_kernel(const __grid_con
       const int col = 2 * t + c;
       // Never 0: a hidden score of -inf stays -inf times it.
       factor[c] = fmaxf(fabsf(p.qk_scale) * pow2(-__shfl_sync(0xFFFFFFFFu, e, 4 * col)), 1.17549435e-38f);
-      const int2 s = col < n_rows ? seen_by(p, rq, (int)query_of(rq, (uint32_t)seg_tile * R + col)) : make_int2(0, rq.hi);
+      const int2 s = col < n_rows ? seen_by(p, rq, (int)query_of_row(p, (uint32_t)seg_tile * R + col)) : make_int2(0, rq.hi);
       lo_q[c] = s.x;
       hi_q[c] = s.y;
       lo_max = max(lo_max, s.x);
@@ -569,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_decode_kernel(const __grid_con
     const bool whole = seg_n == n_units;
     const int part = 2 * (int)blockIdx.x + (first_segment ? 0 : 1);
     auto store_row = [&](int row, int d, float4 o, float mm, float ll) {
-      const uint32_t rr = (uint32_t)seg_tile * R + row, ti = query_of(rq, rr);
+      const uint32_t rr = (uint32_t)seg_tile * R + row, ti = query_of_row(p, rr);
       const int64_t tok = rq.row0 + (int64_t)ti;
       const int head = seg_head * p.group + (int)(rr - ti * p.group);
       const float inv = ll > 0.0f ? p.v_gscale / ll : (ll == 0.0f ? 0.0f : ll);  // a NaN stays one

@@ -44,6 +44,7 @@
 #include "fh_internal.h"
 #include "fh_kv.cuh"
 #include "fh_kv_attn.h"
+#include "fh_nvfp4.cuh"
 
 namespace fh {
 
@@ -301,7 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* raw_live = reinterpret_cast<uint64_t*>(smem + C::kOffRawLive);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
-  int* job_s = reinterpret_cast<int*>(smem + C::kOffMisc + 16);  // request, tile
+  __shared__ Request job_rq;  // the CTA's request, its index and the tile
+  __shared__ int job_s[2];
   __shared__ int scan_s[kThreads / 32];
   __shared__ int last_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -344,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rest < n) {
         job_s[0] = b;
         job_s[1] = rest;
+        job_rq = load_request(p, b);
         break;
       }
       rest -= n;
@@ -383,12 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   Job job;
   job.b = job_s[0];
   job.head = unit % p.kv_heads;
-  job.rq = load_request(p, job.b);
+  job.rq = job_rq;
   job.row0 = job_s[1] * kCtaRows;
   job.n_rows = (int)min((int64_t)kCtaRows, (int64_t)job.rq.n_q * p.group - job.row0);
   {
-    const int lo = seen_by(p, job.rq, job.row0 / p.group).x;
-    const int hi = seen_by(p, job.rq, (job.row0 + job.n_rows - 1) / p.group).y;
+    const int lo = seen_by(p, job.rq, (int)query_of_row(p, (uint32_t)job.row0)).x;
+    const int hi = seen_by(p, job.rq, (int)query_of_row(p, (uint32_t)(job.row0 + job.n_rows - 1))).y;
     const int first = lo / kKeys, n = max(0, (hi + kKeys - 1) / kKeys - first);
     const int from = (int)((int64_t)n * piece / pieces), to = (int)((int64_t)n * (piece + 1) / pieces);
     job.key0 = first + from;
@@ -402,47 +405,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2, r = tid & (kRows - 1);
     const int row = t * kRows + r;
     const bool mine_row = row < job.n_rows;
-    const uint32_t packed = (uint32_t)job.row0 + row, ti = packed / p.group;
+    const uint32_t packed = (uint32_t)job.row0 + row, ti = query_of_row(p, packed);
     const int head = job.head * p.group + (int)(packed - ti * p.group);
     const int64_t tok = job.rq.row0 + (int64_t)ti;
     const int2 see = mine_row ? seen_by(p, job.rq, (int)ti) : make_int2(0, 0);
-    // The warp's 32 rows to FP16, each scaled by a power of two, into the swizzled
-    // Q tile.  kPer lanes take a row together, so that a load covers whole lines
-    // (a row a lane takes 32 lines a load: 4500 cycles a CTA, and as many to store).
+    // The warp's 32 rows into the swizzled Q tile as they are, kPer lanes a row, so
+    // that the copies cover whole lines (a row a lane takes 32 lines a load: 4500
+    // cycles a CTA, and as many to store); then, a row a lane, to FP16 scaled by a
+    // power of two, in place.
     constexpr int kPer = D / 8, kPerLoad = 32 / kPer;  // lanes of a row, rows of a load
     const int64_t q_at = tok * p.ldq + (int64_t)head * D, o_at = tok * p.ldo + (int64_t)head * D;
-    const int piece = lane % kPer;
-    float factor = 0.0f;
+    const int chunk = lane % kPer;
+    auto q_place = [&](int qr, int c) {  // of 16-byte piece c of row qr
+      return C::kOffQ + t * C::kOperand + (c >> 3) * C::kHalfBytes + qr * 128 + (((c & 7) ^ (qr & 7)) * 16);
+    };
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int src = i * kPerLoad + lane / kPer, qr = 32 * (warp & 3) + src;
+      const int64_t at = __shfl_sync(0xFFFFFFFFu, q_at, src);
+      const bool there = t * kRows + qr < job.n_rows;  // zeros else
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sbase + q_place(qr, chunk)),
+                   "l"(p.q + (there ? at + 8 * chunk : 0)), "r"(there ? 16 : 0)
+                   : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    float factor;
     {
       uint4 raw[kPer];
+      uint32_t amax = 0;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int src = i * kPerLoad + lane / kPer;
-        const int64_t at = __shfl_sync(0xFFFFFFFFu, q_at, src);
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (t * kRows + 32 * (warp & 3) + src < job.n_rows) raw[i] = *reinterpret_cast<const uint4*>(p.q + at + 8 * piece);
+        raw[i] = *reinterpret_cast<const uint4*>(smem + q_place(r, i));
+        using nvfp4::max_abs_bf16x2;  // (a NaN is passed over: its own product is one)
+        amax = max_abs_bf16x2(amax, max_abs_bf16x2(max_abs_bf16x2(raw[i].x, raw[i].y), max_abs_bf16x2(raw[i].z, raw[i].w)));
       }
+      const int e = query_exponent(max(amax & 0x7FFFu, (amax >> 16) & 0x7FFFu));
+      // A negative scale goes to the query, so that larger scores are larger sums.
+      const float up = p.qk_scale < 0.0f ? -pow2(e) : pow2(e);
+      // Never 0: a hidden score of -inf stays -inf times it.
+      factor = fmaxf(fabsf(p.qk_scale) * pow2(-e), 1.17549435e-38f);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        uint32_t amax = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) amax = max(amax, max(v[k] & 0x7FFFu, (v[k] >> 16) & 0x7FFFu));
-#pragma unroll
-        for (int o = 1; o < kPer; o <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-        const int e = query_exponent(amax);
-        // A negative scale goes to the query, so that larger scores are larger sums.
-        const float up = p.qk_scale < 0.0f ? -pow2(e) : pow2(e);
         uint32_t h[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(bf16_lo(v[k]) * up, bf16_hi(v[k]) * up);
-        const int qr = 32 * (warp & 3) + i * kPerLoad + lane / kPer;
-        *reinterpret_cast<uint4*>(smem + C::kOffQ + t * C::kOperand + (piece >> 3) * C::kHalfBytes + qr * 128 +
-                                  (((piece & 7) ^ (qr & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
-        // Never 0: a hidden score of -inf stays -inf times it.
-        const float f = fmaxf(fabsf(p.qk_scale) * pow2(-e), 1.17549435e-38f);
-        const float mine = __shfl_sync(0xFFFFFFFFu, f, (lane % kPerLoad) * kPer);
-        if (lane / kPerLoad == i) factor = mine;
+        for (int k = 0; k < 4; ++k) {
+          const float2 x = __fmul2_rn(make_float2(bf16_lo(v[k]), bf16_hi(v[k])), make_float2(up, up));
+          h[k] = pack_f16x2(x.x, x.y);
+        }
+        *reinterpret_cast<uint4*>(smem + q_place(r, i)) = make_uint4(h[0], h[1], h[2], h[3]);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       warp_arrive(qfull, lane);
@@ -626,8 +638,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kPer; ++i) {
           const int src = i * kPerLoad + lane / kPer;
           const int64_t at = __shfl_sync(0xFFFFFFFFu, o_at, src);
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + src * (2 * D) + ((piece ^ (src & 7)) * 16));
-          if (t * kRows + 32 * (warp & 3) + src < job.n_rows) *reinterpret_cast<uint4*>(p.out + at + 8 * piece) = w;
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + src * (2 * D) + ((chunk ^ (src & 7)) * 16));
+          if (t * kRows + 32 * (warp & 3) + src < job.n_rows) *reinterpret_cast<uint4*>(p.out + at + 8 * chunk) = w;
         }
         if (mine_row && p.lse != nullptr)
           p.lse[tok * p.q_heads + head] = l == 0.0f ? -INFINITY : (m - kHead + log2f(l)) * 0.6931471805599453f;
