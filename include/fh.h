@@ -466,7 +466,8 @@ int fh_kv_cache_read(const fh_kv_cache* cache, const int64_t* slots_dev, int64_t
  * q, out: BF16 [total_q, q_heads, head_dim], tokens ldq and ldo elements apart
  * (out must not overlap q).  lens int32 [batch], q_starts int32 [batch + 1],
  * block_table int32 [batch, max_pages]; rows of out and lse that no request has
- * are left as they were.  What the device arrays hold is brought into range, so
+ * are left as they were.  q_starts must not decrease.  What the device arrays
+ * hold is brought into range, so
  * it cannot lead outside a buffer: a table entry that names no page of the
  * cache leaves its tokens out as a mask would, lengths are cut to max_pages *
  * page_size, and rows to total_q.
@@ -483,8 +484,14 @@ int fh_kv_cache_read(const fh_kv_cache* cache, const int64_t* slots_dev, int64_t
  * workspaces of their own.
  * q_heads a multiple of kv_heads, total_q * q_heads < 2^31; ldq, ldo >= q_heads *
  * head_dim, multiples of 8; q, out 16-byte aligned; sm_scale finite; 0 <= window
- * < 2^31; 0 < max_pages, max_pages * page_size < 2^31.  total_q == 0 or
- * batch == 0 enqueues nothing. */
+ * < 2^31; 0 < max_pages, max_pages * page_size <= 2^30.  total_q == 0 or
+ * batch == 0 enqueues nothing.
+ * A bounded wait that expires inside the kernel for many rows sets the device
+ * error word (fh_device_status); the kernel drains what it issued, frees its
+ * TMEM and returns.  Environment (read at each launch): FH_KV_KERNEL=few or
+ * =tiles selects the kernel instead of the estimate; FH_KV_TEST_STALL=1 is a
+ * test hook that makes that kernel's first CTA stop its products after two key
+ * tiles, so that the call ends with FH_ERR_TIMEOUT after about 4 s. */
 int fh_kv_attention(const fh_kv_cache* cache, const uint16_t* q_dev, int64_t total_q, int64_t q_heads, int64_t ldq,
                     const int32_t* block_table_dev, int64_t max_pages, const int32_t* lens_dev,
                     const int32_t* q_starts_dev, int64_t batch, float sm_scale, int causal, int64_t window,

@@ -557,10 +557,10 @@ int fh_kv_attention(const fh_kv_cache* cache, const uint16_t* q_dev, int64_t tot
                 "fh_kv_attention: need q_heads a multiple of kv_heads, total_q * q_heads < 2^31, batch >= 0%s");
   const int64_t row = q_heads * cache->head_dim;
   if (ldq < row || ldo < row || ldq % 8 != 0 || ldo % 8 != 0 || max_pages <= 0 ||
-      max_pages > 0x7FFFFFFF / cache->page_size || window < 0 || window > 0x7FFFFFFF || max_q < 0 || max_kv < 0)
+      max_pages > ((int64_t)1 << 30) / cache->page_size || window < 0 || window > 0x7FFFFFFF || max_q < 0 || max_kv < 0)
     return fail(FH_ERR_UNSUPPORTED_SHAPE,
                 "fh_kv_attention: need ldq and ldo >= q_heads * head_dim and multiples of 8, max_pages > 0, "
-                "max_pages * page_size < 2^31, 0 <= window < 2^31, max_q and max_kv >= 0%s");
+                "max_pages * page_size <= 2^30, 0 <= window < 2^31, max_q and max_kv >= 0%s");
   if (total_q == 0 || batch == 0) return FH_OK;
   if (q_dev == nullptr || block_table_dev == nullptr || lens_dev == nullptr || q_starts_dev == nullptr ||
       out_dev == nullptr || workspace_dev == nullptr)

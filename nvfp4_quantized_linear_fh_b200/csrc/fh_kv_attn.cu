@@ -1,5 +1,6 @@
 // fh_kv_attn.cu -- attention over the paged NVFP4 cache: which kernel takes a call.
 #include <math.h>
+#include <stdlib.h>
 
 #include "fh_internal.h"
 #include "fh_kv_attn.h"
@@ -37,6 +38,8 @@ cudaError_t launch_kv_attention(const fh_kv_cache& c, const KvAttnCall& call, co
   p.num_pages = (int)c.num_pages;
   p.causal = call.causal ? 1 : 0;
   p.window = call.window;
+  const char* stall = getenv("FH_KV_TEST_STALL");  // read at each launch
+  p.stall = stall != nullptr && stall[0] == '1' ? 1 : 0;
   p.qk_scale = (float)((double)call.sm_scale * 1.4426950408889634 * (double)c.k_gscale);
   p.v_gscale = c.v_gscale;
   p.part_o = nullptr;
@@ -50,7 +53,11 @@ cudaError_t launch_kv_attention(const fh_kv_cache& c, const KvAttnCall& call, co
   // 124 / 91; 64 rows of one of 30000, one KV head, 30 / 78.
   int64_t max_kv = shape.max_kv;
   if (p.window > 0 && max_kv > (int64_t)p.window + shape.max_q) max_kv = (int64_t)p.window + shape.max_q;
-  if (shape.max_q * p.group <= kFewRows || kv_attn_split_cost(shape, max_kv) < kv_attn_tiles_cost(shape, max_kv))
+  bool few = shape.max_q * p.group <= kFewRows || kv_attn_split_cost(shape, max_kv) < kv_attn_tiles_cost(shape, max_kv);
+  const char* kernel = getenv("FH_KV_KERNEL");  // read at each launch
+  if (kernel != nullptr && kernel[0] == 'f') few = true;
+  if (kernel != nullptr && kernel[0] == 't') few = false;
+  if (few)
     return launch_kv_attn_split(p, shape, workspace, s);
   return launch_kv_attn_tiles(p, shape, max_kv, workspace, s);
 }

@@ -26,6 +26,7 @@ struct AttnParams {
   int group_shift;
   int page_shift, num_pages;
   int causal, window;
+  int stall;        // test hook: the tile kernel's first CTA stops its products after two key tiles
   float qk_scale;  // sm_scale * log2(e) * k_gscale: scores in units of log2
   float v_gscale;
   // Workspace: partial results of key ranges split over CTAs, and their counters.
@@ -84,8 +85,8 @@ __device__ __forceinline__ int2 seen_by(const AttnParams& p, const Request& r, i
 // nothing else is ever kept there.
 constexpr int kCounters = 1024;
 
-// Up to this many rows (queries x heads of a group) in all, and up to this many a
-// request, always go to the kernel for few rows.
+// Up to this many rows (queries x heads of a group) a request always go to the
+// kernel for few rows.
 constexpr int64_t kFewRows = 32;
 
 // Few rows a request (fh_kv_decode.cu), and tiles of many on the tcgen05 tensor

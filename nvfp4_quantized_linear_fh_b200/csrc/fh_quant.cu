@@ -196,8 +196,8 @@ void build_table(float sg_f, QuantTable* t) {
 
 // Per-thread cache: calibrated layers reuse one s_g for every call, and a model
 // has a few hundred of them (building a table takes far longer than a launch).
-// 512 places found by a hash of the scale's bits; a scale that meets another one
-// in its place is built anew there.
+// 512 places; a scale is looked for in eight of them from a hash of its bits on,
+// and takes the first one's place where all are others'.
 const QuantTable& quant_table_for(float sg) {
   struct Entry {
     float sg;
@@ -213,10 +213,18 @@ const QuantTable& quant_table_for(float sg) {
   thread_local Cache cache;
   uint32_t bits;
   memcpy(&bits, &sg, 4);
-  Entry*& place = cache.at[(bits * 0x9E3779B1u) >> 23];
-  if (place != nullptr && place->sg == sg) return place->t;
-  if (place == nullptr) place = new (std::nothrow) Entry;
-  Entry& e = place != nullptr ? *place : cache.spare;
+  const uint32_t home = (bits * 0x9E3779B1u) >> 23;
+  Entry** place = &cache.at[home];
+  for (uint32_t k = 0; k < 8; ++k) {
+    Entry*& e = cache.at[(home + k) & 511u];
+    if (e == nullptr) {
+      place = &e;
+      break;
+    }
+    if (e->sg == sg) return e->t;
+  }
+  if (*place == nullptr) *place = new (std::nothrow) Entry;
+  Entry& e = *place != nullptr ? **place : cache.spare;
   build_table(sg, &e.t);
   e.sg = sg;
   return e.t;

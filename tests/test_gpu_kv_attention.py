@@ -1,6 +1,9 @@
 """fh_kv_attention against attention in 64 bits over the dequantized cache, with
 the bound of the kernels' roundings (tests/_kv_ref.py), over head layouts,
 lengths, pages, masks and strides; then the whole run of a cache's calls."""
+import contextlib
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -10,6 +13,19 @@ from _gpu_util import bits_of, fh, to_dev
 from _kv_ref import attention, dequantize
 
 pytestmark = pytest.mark.gpu
+
+
+@contextlib.contextmanager
+def selected(kernel):
+    """FH_KV_KERNEL: which kernel takes the calls."""
+    old = os.environ.get("FH_KV_KERNEL")
+    os.environ["FH_KV_KERNEL"] = kernel
+    try:
+        yield
+    finally:
+        os.environ.pop("FH_KV_KERNEL")
+        if old is not None:
+            os.environ["FH_KV_KERNEL"] = old
 
 
 class Case:
@@ -92,9 +108,13 @@ class Case:
         return attention(q, lambda b: of(kv[0], b), lambda b: of(kv[1], b), lens, starts, sm_scale, causal, window, there)
 
     def check(self, sm_scale=None, causal=True, window=0, lens=None, starts=None, **kw):
+        """The call as it chooses its kernel, and with either of the two selected."""
         sm_scale = float(np.float32(self.d ** -0.5)) if sm_scale is None else sm_scale
-        out, lse = self.run(sm_scale, causal=causal, window=window, **kw)
-        compare(out, lse, *self.reference(sm_scale, causal, window, lens, starts))
+        ref = self.reference(sm_scale, causal, window, lens, starts)
+        for kernel in ("", "few", "tiles"):
+            with selected(kernel):
+                out, lse = self.run(sm_scale, causal=causal, window=window, **kw)
+            compare(out, lse, *ref)
         # Every call leaves the workspace's counters zero.
         assert int(self.ws[:4096].view(torch.int32).abs().sum()) == 0
 
@@ -188,13 +208,18 @@ def test_both_kernels_take_turns_on_one_workspace():
     """Calls of few and of many rows, split over CTAs in either way, one after another with one workspace."""
     c = Case([4000, 300], [30, 5], 8, 4, 128, 16, seed=21).device()
     few = Case([4000, 300, 2000], [1, 1, 1], 8, 4, 128, 16, seed=22).device()
-    assert few.ws.numel() <= c.ws.numel()
-    few.ws = c.ws
-    first = c.run(0.09), few.run(0.09)
+    few.ws = c.ws = c.ws if c.ws.numel() > few.ws.numel() else few.ws
+
+    def both():
+        with selected("tiles"):
+            a = c.run(0.09)
+        with selected("few"):
+            return a, few.run(0.09)
+    first = both()
     for _ in range(3):
         c.check()
         few.check()
-        for old, new in zip(first, (c.run(0.09), few.run(0.09))):
+        for old, new in zip(first, both()):
             np.testing.assert_array_equal(old[0], new[0])
             np.testing.assert_array_equal(old[1], new[1])
 
@@ -206,8 +231,14 @@ def test_hints_do_not_change_the_result(max_q, max_kv, n_q):
     c.check(max_q=max_q, max_kv=max_kv)
 
 
+@pytest.fixture(params=["few", "tiles"])
+def kernel(request):
+    with selected(request.param):
+        yield request.param
+
+
 @pytest.mark.parametrize("n_q", [1, 64])
-def test_strided_queries_and_outputs(n_q):
+def test_strided_queries_and_outputs(n_q, kernel):
     """q as the first third of fused QKV rows, out inside a wider buffer whose rest stays as it was."""
     c = Case([100, 260], [n_q, n_q], 6, 3, 64, 16, seed=5).device()
     wide = torch.full((c.T, 6 * 64 + 2 * 3 * 64), float("nan"), dtype=torch.bfloat16, device="cuda")
@@ -243,7 +274,7 @@ def test_scores_that_climb_slowly(n_q):
 
 
 @pytest.mark.parametrize("n_q", [1, 40])
-def test_a_query_row_without_a_value_stays_alone(n_q):
+def test_a_query_row_without_a_value_stays_alone(n_q, kernel):
     """Rows with infinities or NaN come out NaN; all others are as without them."""
     c = Case([150, 80], [n_q, n_q], 4, 2, 128, 16, seed=9).device()
     sm = float(np.float32(0.09))
@@ -258,7 +289,7 @@ def test_a_query_row_without_a_value_stays_alone(n_q):
     np.testing.assert_array_equal(out[~bad], plain[~bad])
 
 
-def test_repeats_are_bit_identical_and_streams_keep_order():
+def test_repeats_are_bit_identical_and_streams_keep_order(kernel):
     c = Case([3000, 17, 800], [1, 1, 1], 16, 4, 128, 16, seed=10).device()
     first = c.run(0.09)
     for _ in range(5):
@@ -273,7 +304,7 @@ def test_repeats_are_bit_identical_and_streams_keep_order():
     np.testing.assert_array_equal(S.bf16_to_f32(bits_of(out)), first[0])
 
 
-def test_pages_past_32_bit_offsets():
+def test_pages_past_32_bit_offsets(kernel):
     """Tokens in pages whose codes lie past 4 GB."""
     m = fh()
     H, d, page, pages = 8, 128, 16, 600_000
@@ -380,5 +411,71 @@ def _serve(graph):
 
 
 @pytest.mark.parametrize("graph", [False, True], ids=["eager", "graph"])
-def test_serving_steps(graph):
+def test_serving_steps(graph, kernel):
     _serve(graph)
+
+
+@pytest.mark.parametrize("L,n_q,heads", [(6000, 60, 2), (600, 600, 64)], ids=["cut", "whole"])
+def test_stall_times_out_and_the_context_survives(L, n_q, heads, monkeypatch):
+    """With the test hook FH_KV_TEST_STALL=1 the first CTA's products stop after two key tiles; its other warps run into
+    their bounded waits, meet, and free TMEM, with its keys cut into pieces (few row tiles) and not; the host reads
+    FH_ERR_TIMEOUT.  Without the hook the same call on the same workspace is right again."""
+    m = fh()
+    m.fh_device_status()
+    c = Case([L], [n_q], heads, heads, 128, 64, seed=2).device()
+    with selected("tiles"):
+        want = c.run(0.09)
+        monkeypatch.setenv("FH_KV_TEST_STALL", "1")
+        with pytest.raises(m.FHError) as e:
+            c.run(0.09)
+        assert e.value.status == m.FH_ERR_TIMEOUT
+        monkeypatch.delenv("FH_KV_TEST_STALL")
+        m.fh_device_status()  # the word was cleared
+        again = c.run(0.09)
+    np.testing.assert_array_equal(want[0], again[0])
+    np.testing.assert_array_equal(want[1], again[1])
+    assert int(c.ws[:4096].view(torch.int32).abs().sum()) == 0
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    """Calls that overlap on the GPU, split over CTAs in both ways, each with its own workspace."""
+    cases = [Case([20000, 900], [1, 1], 8, 2, 128, 16, seed=31).device(), Case([9000], [70], 8, 8, 128, 16, seed=32).device()]
+    forms = ("few", "tiles")
+    want = []
+    for c, form in zip(cases, forms):
+        with selected(form):
+            want.append(c.run(0.09))
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[torch.empty_like(c.t_q) for _ in range(20)] for c in cases]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for c, s, o, form in zip(cases, streams, outs, forms):
+            with selected(form):
+                c.m.fh_kv_attention(c.t_q, c.cache, c.t_table, c.t_lens, c.t_starts, 0.09, o[i], c.ws, stream=s)
+    torch.cuda.synchronize()
+    cases[0].m.fh_device_status()
+    for w, o in zip(want, outs):
+        for x in o:
+            np.testing.assert_array_equal(S.bf16_to_f32(bits_of(x)), w[0])
+
+
+def test_two_graphs_share_a_workspace_in_turns():
+    c = Case([20000, 900], [1, 1], 8, 2, 128, 16, seed=33).device()
+    d = Case([9000], [70], 8, 2, 128, 16, seed=34).device()
+    d.ws = c.ws = d.ws if d.ws.numel() > c.ws.numel() else c.ws
+    want, graphs, outs = [], [], []
+    for x, form in ((c, "few"), (d, "tiles")):
+        with selected(form):
+            want.append(x.run(0.09)[0])
+        out = torch.zeros_like(x.t_q)
+        g = torch.cuda.CUDAGraph()
+        with selected(form), torch.cuda.graph(g):
+            x.m.fh_kv_attention(x.t_q, x.cache, x.t_table, x.t_lens, x.t_starts, 0.09, out, x.ws)
+        graphs.append(g)
+        outs.append(out)
+    for _ in range(4):
+        for g, o, w in zip(graphs, outs, want):
+            o.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            np.testing.assert_array_equal(S.bf16_to_f32(bits_of(o)), w)

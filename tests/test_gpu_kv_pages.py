@@ -154,3 +154,28 @@ def test_unknown_page_gives_no_slot():
     table = np.full((1, 4), -1)
     got = run([5], [20], table, np.array([3, 2, 1]), 3, 16, 20)
     assert got[0] == 0 and (got[6][:11] == -1).all() and got[6][11:15].tolist() == [16, 17, 18, 19]
+
+
+def test_captured_steps_with_many_slots():
+    """The two-launch form captured in a graph, counts and lengths updated in place from replay to replay."""
+    m = fh()
+    rng = np.random.default_rng(6)
+    n, page, cap = 500, 16, 30000
+    state = [np.zeros(n, np.int64), np.full((n, 40), -1, np.int64), rng.permutation(9000), 9000]
+    target, held, table, free, count = i32(state[0]), i32(state[0]), i32(state[1]), i32(state[2]), i32([9000])
+    qs, status, slots = i32(np.zeros(n + 1)), i32([0]), torch.zeros(cap, dtype=torch.int64, device="cuda")
+    call = lambda: m.fh_kv_pages_update(held, target, table, free, count, count, held, qs, slots, status, page)
+    call()  # nothing moves
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for step in range(6):
+        want = np.maximum(0, state[0] + rng.integers(-60, 110, n)).clip(max=600)
+        target.copy_(i32(want))
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = pages_update(state[0], want, state[1], state[2], state[3], page, cap, 40)
+        assert ref[0] == 0 and int(status) == 0
+        for r, g in zip(ref[1:], (table, free, count, held, qs, slots)):
+            np.testing.assert_array_equal(g.cpu().numpy().reshape(np.shape(r)), r)
+        state = [ref[4], ref[1], ref[2], ref[3]]

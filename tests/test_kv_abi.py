@@ -72,7 +72,7 @@ def test_attention_arguments():
     assert attend(c, heads=3) == attend(c, heads=0) == attend(c, heads=1) == attend(c, total_q=-1) == 2
     assert attend(c, batch=-1) == attend(c, total_q=1 << 30) == 2
     assert attend(c, ldq=504) == attend(c, ldo=508) == attend(c, ldo=500) == 2
-    assert attend(c, max_pages=0) == attend(c, max_pages=1 << 28) == attend(c, window=-1) == 2
+    assert attend(c, max_pages=0) == attend(c, max_pages=(1 << 26) + 1) == attend(c, window=-1) == 2
     assert attend(c, window=1 << 31) == attend(c, max_q=-1) == attend(c, max_kv=-1) == 2
     for name in ("q", "table", "lens", "starts", "out", "ws"):
         assert attend(c, **{name: None}) == 1, name
