@@ -484,8 +484,8 @@ int fh_kv_cache_read(const fh_kv_cache* cache, const int64_t* slots_dev, int64_t
  * workspaces of their own.
  * q_heads a multiple of kv_heads, total_q * q_heads < 2^31; ldq, ldo >= q_heads *
  * head_dim, multiples of 8; q, out 16-byte aligned; sm_scale finite; 0 <= window
- * < 2^31; 0 < max_pages, max_pages * page_size <= 2^30.  total_q == 0 or
- * batch == 0 enqueues nothing.
+ * < 2^31; 0 < max_pages, max_pages * page_size <= 2^30; a cache of
+ * at least one page.  total_q == 0 or batch == 0 enqueues nothing.
  * A bounded wait that expires inside the kernel for many rows sets the device
  * error word (fh_device_status); the kernel drains what it issued, frees its
  * TMEM and returns.  Environment (read at each launch): FH_KV_KERNEL=few or

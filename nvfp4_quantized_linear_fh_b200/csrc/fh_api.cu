@@ -562,9 +562,11 @@ int fh_kv_attention(const fh_kv_cache* cache, const uint16_t* q_dev, int64_t tot
                 "fh_kv_attention: need ldq and ldo >= q_heads * head_dim and multiples of 8, max_pages > 0, "
                 "max_pages * page_size <= 2^30, 0 <= window < 2^31, max_q and max_kv >= 0%s");
   if (total_q == 0 || batch == 0) return FH_OK;
+  if (cache->num_pages < 1) return fail(FH_ERR_UNSUPPORTED_SHAPE, "fh_kv_attention: the cache has no page%s");
   if (q_dev == nullptr || block_table_dev == nullptr || lens_dev == nullptr || q_starts_dev == nullptr ||
       out_dev == nullptr || workspace_dev == nullptr)
     return fail(FH_ERR_INVALID_ARG, "fh_kv_attention: null pointer%s");
+  if (out_dev == q_dev) return fail(FH_ERR_INVALID_ARG, "fh_kv_attention: out must not be q%s");
   if (!aligned16(q_dev) || !aligned16(out_dev) || !aligned16(workspace_dev) || !aligned_to(block_table_dev, 4) ||
       !aligned_to(lens_dev, 4) || !aligned_to(q_starts_dev, 4) || !aligned_to(lse_dev, 4))
     return fail(FH_ERR_UNSUPPORTED_SHAPE,

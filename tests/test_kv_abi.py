@@ -38,7 +38,7 @@ def read(c, k=FAKE, v=FAKE, n=4, ldk=256, ldv=256, slots=FAKE):
 
 
 def attend(c, q=FAKE, total_q=4, heads=4, ldq=512, table=FAKE, max_pages=4, lens=FAKE, starts=FAKE, batch=2, scale=1.0,
-           causal=1, window=0, max_q=4, max_kv=64, out=FAKE, ldo=512, lse=None, ws=FAKE, nbytes=1 << 40):
+           causal=1, window=0, max_q=4, max_kv=64, out=2 * FAKE, ldo=512, lse=None, ws=FAKE, nbytes=1 << 40):
     return fh.lib().fh_kv_attention(ctypes.byref(c) if c is not None else None, q, total_q, heads, ldq, table, max_pages,
                                     lens, starts, batch, scale, causal, window, max_q, max_kv, out, ldo, lse, ws, nbytes,
                                     None)
@@ -80,6 +80,8 @@ def test_attention_arguments():
     assert attend(c, table=FAKE + 2) == attend(c, lens=FAKE + 1) == attend(c, starts=FAKE + 3) == 2
     need = fh.fh_kv_attention_workspace_bytes(4, 2, 4, 2, 128)
     assert need > 0 and attend(c, nbytes=need - 1) == 1
+    assert attend(c, out=FAKE) == 1  # q itself
+    assert attend(cache(num_pages=0)) == 2
     assert attend(c, total_q=0, q=None, out=None) == attend(c, batch=0, lens=None) == 0
     assert fh.fh_kv_attention_workspace_bytes(4, 2, 3, 2, 128) == 0
     assert fh.fh_kv_attention_workspace_bytes(4, 2, 4, 2, 80) == 0
