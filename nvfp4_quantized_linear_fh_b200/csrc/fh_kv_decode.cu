@@ -368,11 +368,12 @@ __global__ void __launch_bounds__(kThreads, 3) kv_decode_kernel(const __grid_con
       const uint32_t lv = (live_bits >> (2 * stage)) & 3u;
       const bool edge = lv != 3u || tok0 < lo_max || tok0 + kWarpTokens > hi_min;
       if (lv != 0u && tok0 < rq.hi) {
-        if (tok0 + kWarpTokens > rq.hi) {
-          // Scales behind the last token are whatever the page holds: as zeros
-          // they cannot bring a NaN into sums that weigh them with zero.
+        if (tok0 < rq.lo || tok0 + kWarpTokens > rq.hi) {
+          // Scales in front of the first token seen and behind the last are whatever
+          // the page holds: as zeros they cannot bring a NaN into sums that weigh
+          // them with zero.
           uint8_t* vs = const_cast<uint8_t*>(sb) + St::kOffVs + lane * (D / 16);
-          if (tok0 + lane >= rq.hi) {
+          if (tok0 + lane < rq.lo || tok0 + lane >= rq.hi) {
             if constexpr (D == 128)
               *reinterpret_cast<uint2*>(vs) = make_uint2(0, 0);
             else

@@ -687,8 +687,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = row_in + i * (128 / kCpr);
         codes[i] = *reinterpret_cast<const uint4*>(raw + row * (D / 2) + 16 * part);
         scales[i] = *reinterpret_cast<const uint16_t*>(raw + C::kRawCodes + row * (D / 16) + 2 * part);
-        // Rows of no token get scales of 0, so that nothing of a page's rest gets into a sum.
-        if (!((live >> (8 * (row >> 4))) & 1u) || (job.key0 + j) * kKeys + row >= job.rq.hi) scales[i] = 0;
+        // Rows of no token and of tokens that no query sees get scales of 0, so that nothing of a page's rest,
+        // nor of a page that is no longer the request's, gets into a sum.
+        const int tk = (job.key0 + j) * kKeys + row;
+        if (!((live >> (8 * (row >> 4))) & 1u) || tk < job.rq.lo || tk >= job.rq.hi) scales[i] = 0;
       }
       warp_arrive(rempty(slot), lane);
       ok = warp_wait(is_v ? vempty(s) : kempty(s), ((j / kStages) & 1) ^ 1u, abort_flag);

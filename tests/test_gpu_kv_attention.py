@@ -28,6 +28,12 @@ def selected(kernel):
             os.environ["FH_KV_KERNEL"] = old
 
 
+@pytest.fixture(params=["few", "tiles"])
+def kernel(request):
+    with selected(request.param):
+        yield request.param
+
+
 class Case:
     """A cache of random codes and scales, and requests over it."""
 
@@ -178,6 +184,23 @@ def test_entries_that_name_no_page_are_left_out(n_q):
         c.check(causal=causal, window=window)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n_q,window", [(1, 37), (1, 150), (5, 90), (300, 41)])
+def test_what_lies_before_the_window_does_not_count(n_q, window, d):
+    """NaN scales in every token that no query sees, and in the pages that hold only such tokens entries of other
+    pages, or none."""
+    c = Case([700, 333, 450], [n_q, 1, n_q], 4, 2, d, 32, seed=window, extra_pages=0).poison_tails()
+    for b, L in enumerate(c.lens):
+        unseen = max(0, L - c.n_q[b] - window + 1)
+        for j in range(unseen):
+            for i in (1, 3):
+                c.arrays[i][c.table[b, j // 32], :, j % 32] = 0x7F
+        c.table[b, :unseen // 32] = np.resize([-1, c.table[0, -1], c.pages + 5], unseen // 32)
+    c.device()
+    for causal in (True, False):
+        c.check(causal=causal, window=window)
+
+
 def test_lengths_and_starts_out_of_range_are_cut():
     c = Case([48, 30], [2, 2], 4, 2, 128, 16, seed=4, extra_pages=0).device()
     width = c.width * 16
@@ -229,12 +252,6 @@ def test_both_kernels_take_turns_on_one_workspace():
 def test_hints_do_not_change_the_result(max_q, max_kv, n_q):
     c = Case([900, 400], [n_q, 2], 4, 2, 128, 16, seed=3).device()
     c.check(max_q=max_q, max_kv=max_kv)
-
-
-@pytest.fixture(params=["few", "tiles"])
-def kernel(request):
-    with selected(request.param):
-        yield request.param
 
 
 @pytest.mark.parametrize("n_q", [1, 64])
