@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_decode_kernel(const __grid_con
   f.tile = start_s[1];
   f.head = start_s[2];
   f.unit = start_s[3];
-  int n_left = (int)(u1 - u0), n_fetch = n_left;  // (a piece has at most 2^36 / the CTAs)
+  int n_left = (int)(u1 - u0), n_fetch = n_left;  // (2^31 units would take a CTA a quarter of an hour)
   long long at = u0;  // the line's index of the current unit
 
   // --- fetching: this warp's 32 tokens of a unit into a stage ---------------------

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
   __shared__ Request job_rq;  // the CTA's request, its index and the tile
   __shared__ int job_s[2];
-  __shared__ int scan_s[kThreads / 32];
+  __shared__ long long scan_s[kThreads / 32];
   __shared__ int last_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -316,17 +316,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   const int per = (p.batch + kThreads - 1) / kThreads;
   const int rb0 = min(p.batch, tid * per), rb1 = min(p.batch, rb0 + per);
-  int mine = 0;
+  long long mine = 0;  // (q_starts that decrease can name more rows than there are)
   for (int b = rb0; b < rb1; ++b) mine += tiles_of(b);
-  int incl = mine;
+  long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
     if (lane >= o) incl += v;
   }
   if (lane == 31) scan_s[warp] = incl;
   __syncthreads();
-  int before = incl - mine, total = 0;
+  long long before = incl - mine, total = 0;
   for (int i = 0; i < kThreads / 32; ++i) {
     if (i < warp) before += scan_s[i];
     total += scan_s[i];
@@ -337,15 +337,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int pieces = part_id < 0 ? 1 : cut, piece = part_id < 0 ? 0 : part_id % cut;
   const int cut_unit = part_id < 0 ? 0 : part_id / cut;
   const int unit = part_id < 0 ? (int)blockIdx.x : whole + cut_unit;
-  const int slot = total - 1 - unit / p.kv_heads;
+  const long long slot = total - 1 - unit / p.kv_heads;
   if (slot < 0) return;
   if (slot >= before && slot < before + mine) {
-    int rest = slot - before;
+    long long rest = slot - before;
     for (int b = rb0; b < rb1; ++b) {
       const int n = tiles_of(b);
       if (rest < n) {
         job_s[0] = b;
-        job_s[1] = rest;
+        job_s[1] = (int)rest;
         job_rq = load_request(p, b);
         break;
       }

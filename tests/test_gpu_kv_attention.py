@@ -201,6 +201,15 @@ def test_what_lies_before_the_window_does_not_count(n_q, window, d):
         c.check(causal=causal, window=window)
 
 
+def test_starts_that_decrease_stay_inside_the_buffers(kernel):
+    """Their rows are unspecified; the rows behind them, and the workspace, are as after any call."""
+    c = Case([600, 300, 400], [40, 1, 40], 4, 2, 64, 16, seed=13, gap=2).device()
+    c.t_starts.copy_(torch.tensor([0, 40, 10, 50]))
+    out, lse = c.run(0.1)
+    assert (out[50:] == 9.0).all() and (lse[50:] == 9.0).all() and np.isfinite(out).all()
+    assert int(c.ws[:4096].view(torch.int32).abs().sum()) == 0
+
+
 def test_lengths_and_starts_out_of_range_are_cut():
     c = Case([48, 30], [2, 2], 4, 2, 128, 16, seed=4, extra_pages=0).device()
     width = c.width * 16
