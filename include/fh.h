@@ -460,8 +460,9 @@ int fh_kv_cache_read(const fh_kv_cache* cache, const int64_t* slots_dev, int64_t
  * cached tokens, found through row b of block_table; its queries are its last
  * tokens: query i stands at position lens[b] - n + i of n.  It sees the cached
  * tokens j < lens[b] with, if causal, j <= its position and, if window > 0,
- * j > its position - window.  A query that sees nothing gets out = 0 and
- * lse = -inf.  lse (FP32 [total_q, q_heads], may be NULL) is the natural
+ * j > its position - window.  Pages with no token that one of the request's
+ * queries sees may be gone: what their entries name does not matter.  A query
+ * that sees nothing gets out = 0 and lse = -inf.  lse (FP32 [total_q, q_heads], may be NULL) is the natural
  * logarithm of the softmax's denominator.
  * q, out: BF16 [total_q, q_heads, head_dim], tokens ldq and ldo elements apart
  * (out must not overlap q).  lens int32 [batch], q_starts int32 [batch + 1],

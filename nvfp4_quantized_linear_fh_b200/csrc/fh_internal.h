@@ -137,6 +137,26 @@ cudaError_t launch_adaln_modulation(const uint16_t* e, int64_t bt, int64_t d, co
                                     const uint16_t* proj, const uint16_t* bias, int64_t L, int64_t n, float* code,
                                     float* mod, cudaStream_t s);
 
+// Launches a kernel that begins with griddepcontrol.wait (wait_for_preceding) so
+// that its CTAs are brought up while the preceding kernel of the stream ends.  A
+// layer's cache write and attention for one request of 500 tokens: 9.7 us in a
+// graph and 10.5 launched one by one, 11.5 and 15.5 with plain launches; for 64 of
+// 2000, 50.0 and 51.5, against 50.9 and 54.9.
+template <class... P, class... A>
+cudaError_t launch_overlapping(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The paged NVFP4 key/value cache (fh_kv_pages.cu, fh_kv_cache.cu).  Arguments
 // are validated by the caller.
 cudaError_t launch_kv_pages(const int32_t* held, const int32_t* target, int64_t batch, int64_t page_size,

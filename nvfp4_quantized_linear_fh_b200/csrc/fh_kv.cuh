@@ -15,6 +15,15 @@
 namespace fh {
 namespace kv {
 
+// Nothing that the stream's preceding kernels write may be read, and nothing that
+// they read be written, before this; the next kernel's CTAs may come up from here on.
+// Every thread of a kernel comes here first, so a kernel that has ended says that
+// all before it have, too.
+__device__ __forceinline__ void wait_for_preceding() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Two nibbles (the low one first) of byte `i` of w as FP16 values: E2M1 is a
 // subset of FP16, so the conversion is exact.
 template <int kByte>

@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv_write_kernel(const __grid_co
     for (int i = threadIdx.x; i < (int)(sizeof(QuantTable) / 16); i += kKvThreads) dst[i] = src[i];
   }
   __syncthreads();
+  kv::wait_for_preceding();
   uint32_t clips = 0;
   for (int64_t g = blockIdx.x; g < p.groups; g += gridDim.x) {
     const int64_t t0 = g * p.group;
@@ -167,6 +168,7 @@ template <bool kWide>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_constant__ KvParams p) {
   const KvSide& s = p.side[blockIdx.y];
   const float2 gs = make_float2(s.gscale, s.gscale);
+  kv::wait_for_preceding();
   for (int64_t g = blockIdx.x; g < p.groups; g += gridDim.x) {
     const int64_t t0 = g * p.group;
     const uint32_t n = (uint32_t)min((int64_t)p.group, p.tokens - t0);  // tokens
@@ -272,11 +274,8 @@ cudaError_t launch_kv_write(const fh_kv_cache& c, const uint16_t* k, const uint1
     e.inv6sg = (float)(1.0 / (6.0 * (double)e.gscale));
     e.clip_thr = clip_threshold_bits(e.gscale);
   }
-  if (wide_rows(k, ldk) && wide_rows(v, ldv))
-    kv_write_kernel<true><<<kv_grid(p.k, 2), kKvThreads, 0, s>>>(p);
-  else
-    kv_write_kernel<false><<<kv_grid(p.k, 2), kKvThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  const bool wide = wide_rows(k, ldk) && wide_rows(v, ldv);
+  return launch_overlapping(wide ? kv_write_kernel<true> : kv_write_kernel<false>, kv_grid(p.k, 2), dim3(kKvThreads), 0, s, p);
 }
 
 cudaError_t launch_kv_read(const fh_kv_cache& c, const int64_t* slots, int64_t tokens, uint16_t* k, uint16_t* v,
@@ -292,11 +291,8 @@ cudaError_t launch_kv_read(const fh_kv_cache& c, const int64_t* slots, int64_t t
     p.side[i].inv6sg = 0.0f;
     p.side[i].clip_thr = 0;
   }
-  if (wide_rows(k, ldk) && wide_rows(v, ldv))
-    kv_read_kernel<true><<<kv_grid(p, 16), kKvThreads, 0, s>>>(p);
-  else
-    kv_read_kernel<false><<<kv_grid(p, 16), kKvThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  const bool wide = wide_rows(k, ldk) && wide_rows(v, ldv);
+  return launch_overlapping(wide ? kv_read_kernel<true> : kv_read_kernel<false>, kv_grid(p, 16), dim3(kKvThreads), 0, s, p);
 }
 
 }  // namespace fh

@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_decode_kernel(const __grid_con
   float2* ml_s = reinterpret_cast<float2*>(smem + Sm::kRing + Sm::kO);      // [warp][R]
   const uint32_t ring = smem_addr(smem) + warp * (kStages * St::kBytes);
   const uint8_t* ring_p = smem + warp * (kStages * St::kBytes);
+  wait_for_preceding();
 
   // --- this CTA's piece of the line ------------------------------------------------
   Walk w;
@@ -699,8 +700,7 @@ cudaError_t launch_decode(const AttnParams& p, int64_t ctas, cudaStream_t s) {
   int64_t grid = (int64_t)sm_count() * per_sm;
   if (grid > kMaxCtas) grid = kMaxCtas;
   if (grid > ctas) grid = ctas;
-  kv_decode_kernel<D><<<(int)grid, kThreads, Sm::kBytes, s>>>(p);
-  return cudaGetLastError();
+  return launch_overlapping(kv_decode_kernel<D>, dim3((unsigned)grid), dim3(kThreads), Sm::kBytes, s, p);
 }
 
 }  // namespace

@@ -26,6 +26,7 @@
 #include <stdint.h>
 
 #include "fh_internal.h"
+#include "fh_kv.cuh"
 
 namespace fh {
 
@@ -94,7 +95,6 @@ __device__ __forceinline__ void write_slots(const PagesParams& p, const int32_t*
 }
 
 __global__ void __launch_bounds__(kPagesThreads, 1) kv_pages_kernel(const PagesParams p, bool with_slots) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ int32_t pages_smem[];
   const int n = p.batch;
   int32_t* held_s = pages_smem;          // [n]
@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(kPagesThreads, 1) kv_pages_kernel(const PagesP
   __shared__ int bad_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto cluster = cooperative_groups::this_cluster();
+  kv::wait_for_preceding();
   const int count = *p.free_count;
   if (tid == 0) bad_s = 0;
   __syncthreads();
@@ -233,7 +234,7 @@ constexpr int kSlotThreads = 512;
 // The slots alone, from what kv_pages_kernel has written.
 __global__ void __launch_bounds__(kSlotThreads) kv_slots_kernel(const PagesParams p) {
   extern __shared__ int32_t pages_smem[];  // [batch + 1]
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  kv::wait_for_preceding();
   for (int b = threadIdx.x; b <= p.batch; b += kSlotThreads) pages_smem[b] = p.q_starts[b];
   __syncthreads();
   const int32_t* starts = pages_smem;
@@ -279,7 +280,9 @@ cudaError_t launch_kv_pages(const int32_t* held, const int32_t* target, int64_t 
   // Table entries to write: at most one a request and one a page of new tokens.
   const bool large = batch + slot_capacity / page_size > 1024;
   cudaLaunchConfig_t cfg_a = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = large ? kPagesCtas : 1;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
@@ -288,21 +291,13 @@ cudaError_t launch_kv_pages(const int32_t* held, const int32_t* target, int64_t 
   cfg_a.dynamicSmemBytes = smem;
   cfg_a.stream = s;
   cfg_a.attrs = attr;
-  cfg_a.numAttrs = 1;
+  cfg_a.numAttrs = 2;
   cudaError_t e = cudaLaunchKernelEx(&cfg_a, kv_pages_kernel, p, few);
   if (e != cudaSuccess || few) return e;
   const int64_t runs = (slot_capacity + kRun - 1) / kRun, per_cta = kSlotThreads / 32;
   const int64_t want = (runs + per_cta - 1) / per_cta, cap = (int64_t)sm_count() * 4;
-  cudaLaunchConfig_t cfg_b = {};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg_b.gridDim = dim3((unsigned)(want < cap ? want : cap));
-  cfg_b.blockDim = dim3(kSlotThreads);
-  cfg_b.dynamicSmemBytes = (size_t)(batch + 1) * 4;
-  cfg_b.stream = s;
-  cfg_b.attrs = attr;
-  cfg_b.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg_b, kv_slots_kernel, p);
+  return launch_overlapping(kv_slots_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(kSlotThreads),
+                            (size_t)(batch + 1) * 4, s, p);
 }
 
 }  // namespace fh

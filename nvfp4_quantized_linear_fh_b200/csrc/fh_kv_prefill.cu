@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int last_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  wait_for_preceding();
   // --- which request and rows: the tiles of all requests in one line, the last
   // (under a causal mask the longest) first, heads next to one another ---------------
   constexpr int kCtaRows = kRows * kTiles;
@@ -839,8 +840,8 @@ cudaError_t launch_prefill(const AttnParams& p, int64_t whole, int64_t rest, int
     return e == cudaSuccess ? 1 : -(int)e;
   });
   if (cfg <= 0) return (cudaError_t)(-cfg);
-  kv_prefill_kernel<D><<<(unsigned)(whole + rest * cut), kThreads, C::kSmem, s>>>(p, (int)whole, cut);
-  return cudaGetLastError();
+  return launch_overlapping(kv_prefill_kernel<D>, dim3((unsigned)(whole + rest * cut)), dim3(kThreads), C::kSmem, s, p,
+                            (int)whole, cut);
 }
 
 // As many row tiles (of all KV heads) as there can be: a request's last one may be short.

@@ -505,3 +505,63 @@ def test_two_graphs_share_a_workspace_in_turns():
             g.replay()
             torch.cuda.synchronize()
             np.testing.assert_array_equal(S.bf16_to_f32(bits_of(o)), w)
+
+
+@pytest.mark.parametrize("graph", [False, True], ids=["eager", "graph"])
+def test_a_call_waits_for_its_own_and_for_other_streams(graph, kernel):
+    """Calls launched while the one before still runs: the second one's query is copied in between, the third one's
+    comes from another stream late, and the cache that both read is rewritten behind the second."""
+    c = Case([900, 70], [3, 1], 8, 2, 128, 16, seed=31).device()
+    q2, q3 = c.t_q.flip(0).contiguous(), (c.t_q * 0.5).contiguous()
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn(32, 2, 128, generator=gen, device="cuda").bfloat16() * 0.1 for _ in range(2))
+    at = torch.from_numpy(c.table[0, :2].copy()).cuda()
+    slots = (at[:, None] * 16 + torch.arange(16, device="cuda")).flatten()
+    before = [t.clone() for t in (c.cache.k_codes, c.cache.k_scales, c.cache.v_codes, c.cache.v_scales)]
+
+    def restore():
+        for t, b in zip((c.cache.k_codes, c.cache.k_scales, c.cache.v_codes, c.cache.v_scales), before):
+            t.copy_(b)
+
+    def call(q, out):
+        c.m.fh_kv_attention(q, c.cache, c.t_table, c.t_lens, c.t_starts, 0.1, out, c.ws)
+    outs = [torch.zeros_like(c.t_q) for _ in range(3)]
+    want = [torch.zeros_like(c.t_q) for _ in range(3)]
+    torch.cuda.synchronize()
+    for q, o in ((c.t_q, want[0]), (q2, want[1])):
+        call(q, o)
+        torch.cuda.synchronize()
+    c.m.fh_kv_cache_write(c.cache, k, v, slots)
+    torch.cuda.synchronize()
+    call(q3, want[2])
+    torch.cuda.synchronize()
+    assert not torch.equal(want[2], want[0])
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    q_in, q_late = c.t_q.clone(), torch.zeros_like(c.t_q)
+
+    def run():
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(400000)
+            q_late.copy_(q3)
+        call(q_in, outs[0])
+        q_in.copy_(q2)
+        call(q_in, outs[1])
+        c.m.fh_kv_cache_write(c.cache, k, v, slots)
+        main.wait_stream(side)
+        call(q_late, outs[2])
+    g = torch.cuda.CUDAGraph()
+    if graph:
+        with torch.cuda.graph(g, stream=main):
+            run()
+    for _ in range(3):
+        restore()
+        q_in.copy_(c.t_q)
+        for t in (q_late, *outs):
+            t.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(main):
+            g.replay() if graph else run()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
