@@ -84,14 +84,18 @@ struct Cfg {
   static constexpr int kRawBytes = kRawCodes + kRawScales;
   static constexpr int kOffRaw = kOffV + kStages * kOperand;
   static constexpr int kOffBar = kOffRaw + kRaw * kRawBytes;
-  static constexpr int kBars = 2 * kStages + 4 * kTiles + 4 + 2 * kRaw;
+  // Columns for scores: 128 of a tile each; where there is room a third 128 that the
+  // tiles take in turns, so that a tile's next scores are there when its softmax is
+  // done with the last ones.
+  static constexpr int kBufs = kTiles * (kKeys + D) + kKeys <= 512 ? 3 : 2;
+  static constexpr int kBars = 4 * kStages + 8 * kTiles + 4 + 2 * kRaw;
   static constexpr int kOffLive = kOffBar + 8 * kBars;
   static constexpr int kOffRawLive = kOffLive + 8 * kLive;
   static constexpr int kOffMisc = kOffRawLive + 8 * kRaw;
   // At least half of an SM's shared memory, so that no two CTAs of an SM wait for each other's TMEM.
   static constexpr int kNeed = kOffMisc + 64 + 1024;
   static constexpr int kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
-  static constexpr int kTmemS = 0, kTmemO = kTiles * kKeys;  // column offsets
+  static constexpr int kTmemS = 0, kTmemO = kBufs * kKeys;  // column offsets
   static_assert(kTmemO + kTiles * D <= 512, "TMEM");
   static_assert(kSmem <= 232448, "shared memory");
 };
@@ -284,17 +288,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = s_u32(smem);
   const uint32_t bar0 = sbase + C::kOffBar;
+  constexpr bool kAhead = C::kBufs > kTiles;  // scores run ahead of the softmax
   auto kempty = [&](int s) { return bar0 + 8u * s; };
   auto vempty = [&](int s) { return bar0 + 8u * (kStages + s); };
-  const uint32_t bar1 = bar0 + 16u * kStages;
-  auto sfull = [&](int t) { return bar1 + 8u * t; };                  // scores written
-  auto pfull = [&](int t, int half) { return bar1 + 8u * (kTiles + 2 * t + half); };  // P of 64 keys written
-  auto ofull = [&](int t) { return bar1 + 8u * (3 * kTiles + t); };
-  // Tile 0's first half of P(j) waits for V(j) and K(j + 1) as well: a wait less
+  auto kfull = [&](int s) { return bar0 + 8u * (2 * kStages + s); };  // kAhead
+  auto vfull = [&](int s) { return bar0 + 8u * (3 * kStages + s); };
+  const uint32_t bar1 = bar0 + 32u * kStages;
+  // Scores written, and P of 64 keys written.  Where scores run ahead, steps j and
+  // j + 1 may both be complete before the first of them is waited for: even and odd
+  // steps have barriers of their own.
+  auto sfull = [&](int t, int j) { return bar1 + 8u * (2 * t + (kAhead ? j & 1 : 0)); };
+  auto pfull = [&](int t, int half, int j) { return bar1 + 8u * (2 * kTiles + 4 * t + 2 * half + (kAhead ? j & 1 : 0)); };
+  auto turn = [&](int j) { return (uint32_t)(kAhead ? j >> 1 : j) & 1u; };  // their parity in step j
+  auto ofull = [&](int t) { return bar1 + 8u * (6 * kTiles + t); };
+  auto added = [&](int t) { return bar1 + 8u * (7 * kTiles + t); };  // kAhead: O += P(j) V is done
+  // Else tile 0's first half of P(j) waits for V(j) and K(j + 1) as well: a wait less
   // for the product thread.  K may be there two steps ahead, so that odd steps
   // have a barrier of their own.
-  const uint32_t pfirst_odd = bar1 + 8u * (4 * kTiles);
-  auto pfirst = [&](int j) { return (j & 1) ? pfirst_odd : pfull(0, 0); };
+  const uint32_t pfirst_odd = bar1 + 8u * (8 * kTiles);
+  auto pfirst = [&](int j) { return (j & 1) ? pfirst_odd : pfull(0, 0, 0); };
   const uint32_t qfull = pfirst_odd + 8u, k0full = qfull + 8u, drained = qfull + 16u;
   auto rfull = [&](int i) { return drained + 8u + 8u * i; };
   auto rempty = [&](int i) { return drained + 8u + 8u * (kRaw + i); };
@@ -357,12 +369,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       bar_init(kempty(s), 1);
       bar_init(vempty(s), 1);
+      bar_init(kfull(s), kFeedWarps);
+      bar_init(vfull(s), kFeedWarps);
     }
     for (int t = 0; t < kTiles; ++t) {
-      bar_init(sfull(t), 1);
-      bar_init(pfull(t, 0), t == 0 ? 4 + kFeedWarps : 4);
-      bar_init(pfull(t, 1), 4);
+      for (int j = 0; j < (kAhead ? 2 : 1); ++j) {
+        bar_init(sfull(t, j), 1);
+        bar_init(pfull(t, 0, j), t == 0 && !kAhead ? 4 + kFeedWarps : 4);
+        bar_init(pfull(t, 1, j), 4);
+      }
       bar_init(ofull(t), 1);
+      bar_init(added(t), 1);
     }
     bar_init(pfirst_odd, 4 + kFeedWarps);
     bar_init(qfull, kSoftWarps);
@@ -461,7 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(qfull, lane);
     }
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + lanes + C::kTmemS + t * kKeys, to = tmem + lanes + C::kTmemO + t * D;
+    const uint32_t to = tmem + lanes + C::kTmemO + t * D;
+    int buf = t;  // of the scores
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     if (t < tiles) {
@@ -471,7 +489,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       hi_min = __reduce_min_sync(0xFFFFFFFFu, hi_min);
       float2 sum = make_float2(0.0f, 0.0f);
       for (int j = 0; j < job.n_keys; ++j) {
-        if (!warp_wait(sfull(t), j & 1, abort_flag)) {
+        const uint32_t ts = tmem + lanes + C::kTmemS + buf * kKeys;
+        if constexpr (kAhead) buf = buf + tiles >= C::kBufs ? buf + tiles - C::kBufs : buf + tiles;
+        if (!warp_wait(sfull(t, j), turn(j), abort_flag)) {
           ok = false;
           break;
         }
@@ -516,6 +536,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           sum.x *= keep;
           sum.y *= keep;
           if (j > 0) {
+            if constexpr (kAhead) {
+              // (The scores' commit covers O += P(j - 2) V, so this is the phase waited for.)
+              if (!warp_wait(added(t), (j - 1) & 1, abort_flag)) {
+                ok = false;
+                break;
+              }
+              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            }
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               uint32_t o[16];
@@ -542,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (c & 1) {  // 64 keys' P: the product may start on them
             tmem_stored();
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            warp_arrive(t == 0 && c == 1 ? pfirst(j) : pfull(t, c >> 1), lane);
+            warp_arrive(!kAhead && t == 0 && c == 1 ? pfirst(j) : pfull(t, c >> 1, j), lane);
           }
         }
       }
@@ -701,7 +729,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kPieces; ++i) put(dst, row_in + i * (128 / kCpr), codes[i], scales[i]);
       if (!is_v && x == 0) live_s[j % kLive] = live;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      if (!is_v)
+      if constexpr (kAhead)
+        warp_arrive(is_v ? vfull(s) : kfull(s), lane);
+      else if (!is_v)
         warp_arrive(j == 0 ? k0full : pfirst(j - 1), lane);  // V(j - 1) is there, too
       else if (j + 1 == job.n_keys)
         warp_arrive(pfirst(j), lane);
@@ -710,53 +740,96 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kMmaWarp) {
     // ===================== the products =====================
-    auto scores = [&](int t, int s) {  // S_t = Q_t K^T
+    auto scores = [&](int t, int buf, int s) {  // S_t = Q_t K^T
       const uint64_t a = sw128_desc(sbase + C::kOffQ + t * C::kOperand, 16);
       const uint64_t b = sw128_desc(sbase + C::kOffK + s * C::kOperand, 16);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t step = (k >> 2) * C::kHalfBytes + (k & 3) * 32;
-        mma_ss(tmem + C::kTmemS + t * kKeys, desc_add(a, step), desc_add(b, step), idesc(kKeys, false), k > 0);
+        mma_ss(tmem + C::kTmemS + buf * kKeys, desc_add(a, step), desc_add(b, step), idesc(kKeys, false), k > 0);
       }
     };
-    auto output = [&](int t, int s, int half, bool accumulate) {  // O_t += P_t V over 64 keys
+    auto output = [&](int t, int buf, int s, int half, bool accumulate) {  // O_t += P_t V over 64 keys
       const uint64_t b = sw128_desc(sbase + C::kOffV + s * C::kOperand, C::kHalfBytes);
 #pragma unroll
       for (int k = 4 * half; k < 4 * half + 4; ++k)
-        mma_ts(tmem + C::kTmemO + t * D, tmem + C::kTmemS + t * kKeys + 8 * k, desc_add(b, k * 2048),
+        mma_ts(tmem + C::kTmemO + t * D, tmem + C::kTmemS + buf * kKeys + 8 * k, desc_add(b, k * 2048),
                idesc(D, true), accumulate || k > 0);
     };
     if (elect()) {  // one thread waits and issues: no votes between a wait and its product
-      bool ok = job.n_keys > 0 && bar_wait(qfull, 0, abort_flag) && bar_wait(k0full, 0, abort_flag);
-      if (ok) {
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        for (int t = 0; t < tiles; ++t) {
-          scores(t, 0);
-          commit(sfull(t));
-        }
-        commit(kempty(0));
-      }
-      for (int j = 0; j < job.n_keys && ok; ++j) {
-        if (p.stall && blockIdx.x == 0 && j == 2) break;  // test hook: the others run into their bounded waits
-        const int s = j % kStages, sn = (j + 1) % kStages;
-        const bool more = j + 1 < job.n_keys;
-        for (int t = 0; t < tiles && ok; ++t) {
-          ok = t == 0 ? bar_wait(pfirst(j), (j >> 1) & 1, abort_flag) : bar_wait(pfull(t, 0), j & 1, abort_flag);
-          if (!ok) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          output(t, s, 0, j > 0);
-          ok = bar_wait(pfull(t, 1), j & 1, abort_flag);
-          if (!ok) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          output(t, s, 1, true);
-          if (!more) commit(ofull(t));
-          if (more) {
-            scores(t, sn);
-            commit(sfull(t));
+      if constexpr (kAhead) {
+        // In the order (tile 0, tile 1) of step 0, of step 1, ...; scores are tiles + 1
+        // places ahead of outputs, in the columns that the last output has read P from.
+        const int n_all = job.n_keys * tiles;
+        int s_n = 0, s_j = 0, s_t = 0, s_buf = 0;
+        auto next_scores = [&]() {
+          if (s_t == 0) {
+            if (!bar_wait(kfull(s_j % kStages), (s_j / kStages) & 1, abort_flag)) return false;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           }
-          if (t == tiles - 1) {
-            commit(vempty(s));
-            if (more) commit(kempty(sn));
+          scores(s_t, s_buf, s_j % kStages);
+          commit(sfull(s_t, s_j));
+          if (s_t == tiles - 1) commit(kempty(s_j % kStages));
+          s_buf = s_buf + 1 == C::kBufs ? 0 : s_buf + 1;
+          if (++s_t == tiles) s_t = 0, ++s_j;
+          ++s_n;
+          return true;
+        };
+        bool ok = n_all > 0 && bar_wait(qfull, 0, abort_flag);
+        while (ok && s_n < min(tiles + 1, n_all)) ok = next_scores();
+        int buf = 0;
+        for (int j = 0; j < job.n_keys && ok; ++j) {
+          if (p.stall && blockIdx.x == 0 && j == 2) break;  // test hook: the others run into their bounded waits
+          const int s = j % kStages;
+          for (int t = 0; t < tiles && ok; ++t) {
+            ok = bar_wait(pfull(t, 0, j), turn(j), abort_flag) &&
+                 (t > 0 || bar_wait(vfull(s), (j / kStages) & 1, abort_flag));
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            output(t, buf, s, 0, j > 0);
+            ok = bar_wait(pfull(t, 1, j), turn(j), abort_flag);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            output(t, buf, s, 1, true);
+            commit(added(t));
+            if (j + 1 == job.n_keys) commit(ofull(t));
+            if (t == tiles - 1) commit(vempty(s));
+            buf = buf + 1 == C::kBufs ? 0 : buf + 1;
+            if (s_n < n_all) ok = next_scores();
+          }
+        }
+      } else {
+        bool ok = job.n_keys > 0 && bar_wait(qfull, 0, abort_flag) && bar_wait(k0full, 0, abort_flag);
+        if (ok) {
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          for (int t = 0; t < tiles; ++t) {
+            scores(t, t, 0);
+            commit(sfull(t, 0));
+          }
+          commit(kempty(0));
+        }
+        for (int j = 0; j < job.n_keys && ok; ++j) {
+          if (p.stall && blockIdx.x == 0 && j == 2) break;  // test hook: the others run into their bounded waits
+          const int s = j % kStages, sn = (j + 1) % kStages;
+          const bool more = j + 1 < job.n_keys;
+          for (int t = 0; t < tiles && ok; ++t) {
+            ok = t == 0 ? bar_wait(pfirst(j), (j >> 1) & 1, abort_flag) : bar_wait(pfull(t, 0, j), j & 1, abort_flag);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            output(t, t, s, 0, j > 0);
+            ok = bar_wait(pfull(t, 1, j), j & 1, abort_flag);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            output(t, t, s, 1, true);
+            if (!more) commit(ofull(t));
+            if (more) {
+              scores(t, t, sn);
+              commit(sfull(t, j + 1));
+            }
+            if (t == tiles - 1) {
+              commit(vempty(s));
+              if (more) commit(kempty(sn));
+            }
           }
         }
       }
