@@ -575,7 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       l = sum.x + sum.y;
-      if (ok && job.n_keys > 0) ok = warp_wait(ofull(t), 0, abort_flag);
+      // (Without keys no product has waited for the other warps' queries, over which the output is staged.)
+      if (ok) ok = warp_wait(job.n_keys > 0 ? ofull(t) : qfull, 0, abort_flag);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       float weight[kMaxPieces];  // of the pieces' partial outputs
       if (pieces > 1) {  // (also when a wait has run out: all of these warps meet at the barriers)
