@@ -321,51 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   wait_for_preceding();
-  // --- which request and rows: the tiles of all requests in one line, the last
-  // (under a causal mask the longest) first, heads next to one another ---------------
-  constexpr int kCtaRows = kRows * kTiles;
-  auto tiles_of = [&](int b) {
-    return (int)(((int64_t)load_request(p, b).n_q * p.group + kCtaRows - 1) / kCtaRows);
-  };
-  const int per = (p.batch + kThreads - 1) / kThreads;
-  const int rb0 = min(p.batch, tid * per), rb1 = min(p.batch, rb0 + per);
-  long long mine = 0;  // (q_starts that decrease can name more rows than there are)
-  for (int b = rb0; b < rb1; ++b) mine += tiles_of(b);
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) scan_s[warp] = incl;
-  __syncthreads();
-  long long before = incl - mine, total = 0;
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) before += scan_s[i];
-    total += scan_s[i];
-  }
-  // The first `whole` CTAs have a row tile of a KV head each, the others a piece
-  // of one cut into `cut`.
-  const int part_id = (int)blockIdx.x - whole;  // place of the partial result
-  const int pieces = part_id < 0 ? 1 : cut, piece = part_id < 0 ? 0 : part_id % cut;
-  const int cut_unit = part_id < 0 ? 0 : part_id / cut;
-  const int unit = part_id < 0 ? (int)blockIdx.x : whole + cut_unit;
-  const long long slot = total - 1 - unit / p.kv_heads;
-  if (slot < 0) return;
-  if (slot >= before && slot < before + mine) {
-    long long rest = slot - before;
-    for (int b = rb0; b < rb1; ++b) {
-      const int n = tiles_of(b);
-      if (rest < n) {
-        job_s[0] = b;
-        job_s[1] = (int)rest;
-        job_rq = load_request(p, b);
-        break;
-      }
-      rest -= n;
-    }
-  }
-  if (tid == 0) {
+  // (The barriers and TMEM while the others' loads are on their way.)
+  if (tid == 32 * (kMmaWarp + 2)) {
     for (int s = 0; s < kStages; ++s) {
       bar_init(kempty(s), 1);
       bar_init(vempty(s), 1);
@@ -397,6 +354,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                  "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  // --- which request and rows: the tiles of all requests in one line, the last
+  // (under a causal mask the longest) first, heads next to one another ---------------
+  constexpr int kCtaRows = kRows * kTiles;
+  auto tiles_of = [&](const Request& r) { return (int)(((int64_t)r.n_q * p.group + kCtaRows - 1) / kCtaRows); };
+  const int per = (p.batch + kThreads - 1) / kThreads;
+  const int rb0 = min(p.batch, tid * per), rb1 = min(p.batch, rb0 + per);
+  long long mine = 0;  // (q_starts that decrease can name more rows than there are)
+  Request rq;
+  for (int b = rb0; b < rb1; ++b) {
+    rq = load_request(p, b);
+    mine += tiles_of(rq);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scan_s[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) before += scan_s[i];
+    total += scan_s[i];
+  }
+  // The first `whole` CTAs have a row tile of a KV head each, the others a piece
+  // of one cut into `cut`.
+  const int part_id = (int)blockIdx.x - whole;  // place of the partial result
+  const int pieces = part_id < 0 ? 1 : cut, piece = part_id < 0 ? 0 : part_id % cut;
+  const int cut_unit = part_id < 0 ? 0 : part_id / cut;
+  const int unit = part_id < 0 ? (int)blockIdx.x : whole + cut_unit;
+  const long long slot = total - 1 - unit / p.kv_heads;
+  if (slot < 0) {
+    if (warp == kMmaWarp)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot), "r"(512));
+    return;
+  }
+  if (slot >= before && slot < before + mine) {
+    long long rest = slot - before;
+    for (int b = rb0; b < rb1; ++b) {
+      if (per > 1) rq = load_request(p, b);
+      const int n = tiles_of(rq);
+      if (rest < n) {
+        job_s[0] = b;
+        job_s[1] = (int)rest;
+        job_rq = rq;
+        break;
+      }
+      rest -= n;
+    }
+  }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -411,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lo = seen_by(p, job.rq, (int)query_of_row(p, (uint32_t)job.row0)).x;
     const int hi = seen_by(p, job.rq, (int)query_of_row(p, (uint32_t)(job.row0 + job.n_rows - 1))).y;
     const int first = lo / kKeys, n = max(0, (hi + kKeys - 1) / kKeys - first);
-    const int from = (int)((int64_t)n * piece / pieces), to = (int)((int64_t)n * (piece + 1) / pieces);
+    const int from = (uint32_t)(n * piece) / (uint32_t)pieces, to = (uint32_t)(n * (piece + 1)) / (uint32_t)pieces;
     job.key0 = first + from;
     job.n_keys = to - from;
   }
@@ -846,16 +854,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool is_scale = lane & 8;
       const uint32_t per_token = is_scale ? D / 16 : D / 2;
       const bool mine_piece = lane < 16 && piece < (kKeys >> shift);
-      auto look_up = [&](int j) {  // the piece's page, -1 where there is none or nothing to read
+      const int32_t* row = p.table + (int64_t)job.b * p.max_pages;
+      auto look_up = [&](int j) {  // the entry of the piece's page, -1 where there is nothing to read
         const int tk = (job.key0 + j) * kKeys + (piece << shift);
-        if (!mine_piece || j >= job.n_keys || tk >= job.rq.hi) return -1;
-        const int page = p.table[(int64_t)job.b * p.max_pages + (tk >> p.page_shift)];
-        return page < p.num_pages ? page : -1;
+        return mine_piece && j < job.n_keys && tk < job.rq.hi ? row[tk >> p.page_shift] : -1;
       };
-      int page = look_up(0);
+      int entry = look_up(0);
       int issued = 0;
       for (int j = 0; j < job.n_keys; ++j) {
-        const int next = look_up(j + 1);
+        const int page = entry < p.num_pages ? entry : -1;
+        entry = look_up(j + 1);  // (not looked at before the next step)
         const int tk = (job.key0 + j) * kKeys + (piece << shift);
         const int tokens = page >= 0 ? min(1 << shift, (job.rq.hi - tk + 15) & ~15) : 0;
         const int64_t at = page >= 0 ? (((int64_t)page * p.kv_heads + job.head) << p.page_shift) + (tk & ((1 << p.page_shift) - 1)) : 0;
@@ -886,7 +894,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++issued;
         }
         if (!ok) break;
-        page = next;
       }
       // Copies in flight end before the CTA does.
       for (int n = max(0, issued - kRaw); n < issued; ++n) bar_drain(rfull(n % kRaw), (n / kRaw) & 1);
