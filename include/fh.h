@@ -368,7 +368,9 @@ int fh_adaln_modulation(const uint16_t* temb_dev, int64_t bt, int64_t d, const u
  *                       element 2j of a head in the low nibble of byte j
  *   k_scales, v_scales  [num_pages, kv_heads, page_size, head_dim / 16] E4M3
  *   k_gscale, v_gscale  the tensors' FP32 scales, finite and > 0
- * with k ~ code * scale * k_gscale, and v likewise.  The memory is the
+ * with k ~ code * scale * k_gscale, and v likewise.  (fh_kv_cache_write writes
+ * no NaN scale, 0x7F or 0xFF.  One that the caller puts into a token seen by any
+ * of a request's queries may make all of that request's outputs NaN.)  The memory is the
  * caller's; the struct is read during a call only.  A token's SLOT is
  * page * page_size + its place in the page.
  * page_size: a power of two, 16 .. 1024.  head_dim: 64 or 128.  kv_heads:

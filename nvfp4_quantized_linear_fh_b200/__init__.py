@@ -450,7 +450,8 @@ class _CKVCache(_c.Structure):
 class KVCache:
     """One attention layer's keys and values in pages of NVFP4 tokens (fh_kv_cache in include/fh.h): uint8 codes
     [pages, kv_heads, page_size, head_dim / 2] and E4M3 scales [pages, kv_heads, page_size, head_dim / 16] of each,
-    contiguous on one device, and their FP32 scales.  Holds the tensors; empty_kv_cache makes new ones."""
+    contiguous on one device, and their FP32 scales.  Holds the tensors; empty_kv_cache makes new ones.  Its
+    attributes are fixed: calls read the C struct that was filled from them."""
 
     def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
                  k_gscale: float, v_gscale: float):
@@ -471,6 +472,11 @@ class KVCache:
                             self.num_pages, self.page_size, self.kv_heads, self.head_dim, self.k_gscale,
                             self.v_gscale)
         self._ref = _P(_c.addressof(self._c))
+
+    def __setattr__(self, name, value):
+        if "_ref" in self.__dict__:
+            raise AttributeError(f"KVCache.{name} is fixed; make another KVCache of the tensors")
+        super().__setattr__(name, value)
 
 
 def empty_kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, k_gscale: float, v_gscale: float,

@@ -170,3 +170,12 @@ def test_empty_calls_and_other_stream():
     oc, osc, _ = oracle.quantize(np.full((1, 64), 0x3F80, np.uint16), 1.0)
     want = S.to_bf16_bits(dequantize(oc, osc, 1.0))
     np.testing.assert_array_equal(bits_of(back).reshape(2, 64), np.repeat(want, 2, 0))
+
+
+def test_a_cache_keeps_what_it_was_made_of():
+    """Calls read the C struct that was filled from the attributes, so none of them can be set afterwards."""
+    cache = fh().empty_kv_cache(2, 16, 2, 64, 1.0, 1.0)
+    for name, value in (("k_gscale", 2.0), ("v_codes", cache.v_codes.clone()), ("page_size", 32)):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, value)
+    assert cache.k_gscale == 1.0 and cache.page_size == 16
