@@ -236,6 +236,26 @@ def test_few_rows_over_many_keys(lens, n_q, Hq, Hk, d):
         c.check(causal=causal, window=window)
 
 
+@pytest.mark.parametrize("n,Hq,Hk,d", [(700, 3, 1, 64), (1100, 2, 2, 128)])
+def test_many_requests(n, Hq, Hk, d):
+    """More requests than a CTA has threads, some without queries or tokens, one among them of many rows."""
+    i = np.arange(n)
+    lens, n_q = i * 7 % 41, np.where(i % 5 == 3, 0, i % 4)
+    lens[n // 2], n_q[n // 2] = 400, 130
+    c = Case(lens, n_q, Hq, Hk, d, 16, seed=n, gap=1).poison_tails().device()
+    c.check()
+    c.check(causal=False, window=9)
+
+
+@pytest.mark.parametrize("lens,n_q,Hq,Hk,d", [([70, 9], [1, 2], 72, 1, 64), ([45, 200], [3, 1], 130, 2, 128),
+                                              ([5], [1], 4096, 4096, 64), ([40], [1], 1000, 1000, 128)])
+def test_many_heads(lens, n_q, Hq, Hk, d):
+    """Groups that are no power of two and larger than a tile's rows, and as many heads as a cache may have."""
+    c = Case(lens, n_q, Hq, Hk, d, 16, seed=Hq).poison_tails().device()
+    c.check()
+    c.check(causal=False, window=7)
+
+
 def test_both_kernels_take_turns_on_one_workspace():
     """Calls of few and of many rows, split over CTAs in either way, one after another with one workspace."""
     c = Case([4000, 300], [30, 5], 8, 4, 128, 16, seed=21).device()
