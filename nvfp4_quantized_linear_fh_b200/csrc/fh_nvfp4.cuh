@@ -23,7 +23,10 @@
 namespace fh {
 
 struct __align__(16) QuantTable {
-  uint16_t code_thr[128][8];  // [c][j<7]: smallest |x| (BF16 bits) whose exact magnitude code is >= j+1 at scale code c
+  // [c][j<7]: smallest |x| (BF16 bits) whose exact magnitude code is >= j+1 at scale code c.
+  // [c][7]: BF16 bits of the multiplier's rest, 1 / (S_c * s_g) less the FP32 in sc[c].x, where the
+  //      converter is exact on x times the two but not on x times the first; else +Inf bits.
+  uint16_t code_thr[128][8];
   // Per scale code c, everything one block needs in one 8-byte load:
   //   x: the FP32 bits of 1 / (S_c * s_g), the multiplier of the converter path
   //      (0 for c == 0);
@@ -52,29 +55,6 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
 
 __device__ __forceinline__ float bf16_to_float(uint32_t bits16) { return __uint_as_float(bits16 << 16); }
 
-// 16 BF16 values (words w0..w7 in q0, q1) -> 8 code bytes, exact-threshold path.
-// Out of line: only blocks whose scale code failed the converter check get here.
-static __device__ __noinline__ uint2 codes_exact(const QuantTable& t, uint32_t c, uint4 q0, uint4 q1) {
-  const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-  uint32_t thr[7];
-#pragma unroll
-  for (int j = 0; j < 7; ++j) thr[j] = t.code_thr[c][j];
-  uint32_t out[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t lo = w[i] & 0xFFFFu, hi = w[i] >> 16;
-    uint32_t ml = 0, mh = 0;
-#pragma unroll
-    for (int j = 0; j < 7; ++j) {
-      ml += ((lo & 0x7FFFu) >= thr[j]) ? 1u : 0u;
-      mh += ((hi & 0x7FFFu) >= thr[j]) ? 1u : 0u;
-    }
-    const uint32_t byte = (ml | ((lo >> 12) & 8u)) | ((mh | ((hi >> 12) & 8u)) << 4);
-    out[i >> 2] |= byte << (8 * (i & 3));
-  }
-  return make_uint2(out[0], out[1]);
-}
-
 // Four BF16 words (8 values) -> 4 code bytes (low value in the low nibble);
 // the products x * inv are formed two at a time (mul.rn.f32x2: IEEE
 // round-to-nearest per lane, no flush to zero, the same as a scalar multiply).
@@ -96,6 +76,61 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(float inv, uint32_t w0, uint32_t 
         "f"(__uint_as_float(w2 << 16)), "f"(__uint_as_float(w2 & 0xFFFF0000u)),
         "f"(__uint_as_float(w3 << 16)), "f"(__uint_as_float(w3 & 0xFFFF0000u)), "f"(inv));
   return r;
+}
+
+// The same with a multiplier of two parts: x * inv + x * lo, rounded once (and
+// x * lo before it, by 2^-24 of 2^-24).
+__device__ __forceinline__ uint32_t cvt_e2m1x8_rest(float inv, float lo, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+  uint32_t r;
+  asm("{\n\t.reg .b64 s, r, a0, a1, a2, a3, b0, b1, b2, b3;\n\t.reg .f32 l0, h0, l1, h1, l2, h2, l3, h3;\n\t.reg .b8 t0, t1, t2, t3;\n\t"
+      "mov.b64 s, {%9, %9};\n\tmov.b64 r, {%10, %10};\n\t"
+      "mov.b64 a0, {%1, %2};\n\tmov.b64 a1, {%3, %4};\n\tmov.b64 a2, {%5, %6};\n\tmov.b64 a3, {%7, %8};\n\t"
+      "mul.rn.f32x2 b0, a0, r;\n\tmul.rn.f32x2 b1, a1, r;\n\tmul.rn.f32x2 b2, a2, r;\n\tmul.rn.f32x2 b3, a3, r;\n\t"
+      "fma.rn.f32x2 a0, a0, s, b0;\n\tfma.rn.f32x2 a1, a1, s, b1;\n\tfma.rn.f32x2 a2, a2, s, b2;\n\tfma.rn.f32x2 a3, a3, s, b3;\n\t"
+      "mov.b64 {l0, h0}, a0;\n\tmov.b64 {l1, h1}, a1;\n\tmov.b64 {l2, h2}, a2;\n\tmov.b64 {l3, h3}, a3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t0, h0, l0;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t1, h1, l1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t2, h2, l2;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t3, h3, l3;\n\t"
+      "mov.b32 %0, {t0, t1, t2, t3};\n\t}"
+      : "=r"(r)
+      : "f"(__uint_as_float(w0 << 16)), "f"(__uint_as_float(w0 & 0xFFFF0000u)),
+        "f"(__uint_as_float(w1 << 16)), "f"(__uint_as_float(w1 & 0xFFFF0000u)),
+        "f"(__uint_as_float(w2 << 16)), "f"(__uint_as_float(w2 & 0xFFFF0000u)),
+        "f"(__uint_as_float(w3 << 16)), "f"(__uint_as_float(w3 & 0xFFFF0000u)), "f"(inv), "f"(lo));
+  return r;
+}
+
+// The codes of blocks whose scale code failed the converter check: 16 BF16 values
+// (words w0..w7 in q0, q1) -> 8 code bytes.  Out of line.  With an s_g of few
+// significant bits (1, say) quotients lie on the borders between two codes, and a
+// single multiplier puts some of them beside; one of two parts puts them there:
+// 32768 tokens x 21 heads x 128 are written in 111 us at s_g = 1, in 224 by thresholds alone.
+static __device__ __noinline__ uint2 codes_exact(const QuantTable& t, uint32_t c, float amax, uint4 q0, uint4 q1) {
+  const uint32_t rest = t.code_thr[c][7];
+  const float inv = __uint_as_float(t.sc[c].x);
+  if (rest != 0x7F80u && amax * inv <= 3.0e38f) {
+    const float lo = bf16_to_float(rest);
+    return make_uint2(cvt_e2m1x8_rest(inv, lo, q0.x, q0.y, q0.z, q0.w), cvt_e2m1x8_rest(inv, lo, q1.x, q1.y, q1.z, q1.w));
+  }
+  const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+  uint32_t thr[7];
+#pragma unroll
+  for (int j = 0; j < 7; ++j) thr[j] = t.code_thr[c][j];
+  uint32_t out[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t lo = w[i] & 0xFFFFu, hi = w[i] >> 16;
+    uint32_t ml = 0, mh = 0;
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+      ml += ((lo & 0x7FFFu) >= thr[j]) ? 1u : 0u;
+      mh += ((hi & 0x7FFFu) >= thr[j]) ? 1u : 0u;
+    }
+    const uint32_t byte = (ml | ((lo >> 12) & 8u)) | ((mh | ((hi >> 12) & 8u)) << 4);
+    out[i >> 2] |= byte << (8 * (i & 3));
+  }
+  return make_uint2(out[0], out[1]);
 }
 
 // One 16-element block, BF16 words w[0..7] (element 2i in the low half of
@@ -122,7 +157,7 @@ __device__ __forceinline__ uint32_t quantize_block_codes(const QuantTable& tab, 
   if (((e.y >> 15) & 1u) && (amax_f * inv <= 3.0e38f)) {
     codes = make_uint2(cvt_e2m1x8(inv, w[0], w[1], w[2], w[3]), cvt_e2m1x8(inv, w[4], w[5], w[6], w[7]));
   } else {
-    codes = codes_exact(tab, c, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+    codes = codes_exact(tab, c, amax_f, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
   }
   amax_bits = amax;
   return c;

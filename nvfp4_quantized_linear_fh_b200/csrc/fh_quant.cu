@@ -147,18 +147,19 @@ void build_table(float sg_f, QuantTable* t) {
   // BF16 range.  Negative inputs give the same magnitude with the sign bit set.
   // When the FP32 product of a boundary value lands on a midpoint the nearest
   // multiplier fails the check; a neighbouring FP32 multiplier usually passes,
-  // so up to two on each side are tried before the code falls back to the
-  // exact threshold path.
+  // so up to two on each side are tried before the code falls back to a
+  // multiplier of two parts, and to the exact threshold path behind it.
   for (int c = 0; c < 127; ++c) {
     auto exact_mag = [&](uint32_t a) {
       uint32_t m = 0;
       for (int j = 0; j < 7; ++j) m += (a >= t->code_thr[c][j]) ? 1u : 0u;
       return m;
     };
-    auto passes = [&](float inv) {
+    auto passes = [&](float inv, float rest) {
       bool ok = true;
       auto probe = [&](uint32_t a) {
-        const float y = bf16_bits_value(a) * inv;  // the kernel's FP32 multiply
+        const float x = bf16_bits_value(a);
+        const float y = rest == 0.0f ? x * inv : fmaf(x, inv, x * rest);  // as the kernel's FP32 operations
         ok = ok && converter_e2m1(y) == exact_mag(a);
       };
       probe(0);
@@ -176,11 +177,19 @@ void build_table(float sg_f, QuantTable* t) {
     const float up1 = nextafterf(inv0, INFINITY), dn1 = nextafterf(inv0, 0.0f);
     const float cand[5] = {inv0, up1, dn1, nextafterf(up1, INFINITY), nextafterf(dn1, 0.0f)};
     for (float m : cand) {
-      if (passes(m)) {
+      if (passes(m, 0.0f)) {
         inv[c] = m;
         fast_ok[c] = true;
         break;
       }
+    }
+    // Else the multiplier in two parts, the second one a BF16.
+    if (!fast_ok[c] && c != 0 && isfinite(inv0)) {
+      const float rest = (float)(1.0 / (e4m3_magnitude(c) * sg) - (double)inv0);
+      uint32_t bits;
+      memcpy(&bits, &rest, 4);
+      bits &= 0xFFFF0000u;  // cut: 2^-7 of what is 2^-24 of the multiplier
+      if (bits != 0 && passes(inv0, bf16_bits_value(bits >> 16))) t->code_thr[c][7] = (uint16_t)(bits >> 16);
     }
   }
   // The packed per-code entries the kernels read.

@@ -119,6 +119,21 @@ def test_edge_values():
     check(8, 2, 64, 16, 3, k=S.to_bf16_bits(x), v=S.to_bf16_bits(-x), gscales=(1.0, 0.37))
 
 
+@pytest.mark.parametrize("sg", [1.0, 0.0078125, 1.5, 1.25, 3.0, 0.1])
+def test_borders_at_every_block_scale(sg):
+    """Elements on the borders between two codes and next to them, at each of the 126 block scales: where s_g has few
+    significant bits the borders are BF16 values, and ties."""
+    s = np.arange(1, 127)
+    s = np.where(s < 8, s * 2.0 ** -9, (8 + s % 8) * 2.0 ** (s // 8 - 10.0))
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    at = S.to_bf16_bits((s[:, None] * sg * mids).astype(np.float32)).astype(np.int64)  # [126, 7]
+    near = np.concatenate([at, at - 1, at + 1], 1)
+    near = np.concatenate([near, near | 0x8000, near[:, :18]], 1).reshape(126, 4, 15)
+    top = np.broadcast_to(S.to_bf16_bits((6 * s * sg).astype(np.float32)).astype(np.int64)[:, None, None], (126, 4, 1))
+    x = np.concatenate([top, near], 2).reshape(126, 1, 64).astype(np.uint16)
+    check(126, 1, 64, 32, 9, k=x, v=x ^ 0x8000, gscales=(sg, sg))
+
+
 def test_many_scales_take_turns():
     """More global scales than a table cache holds in one place, in turns: each call uses its own."""
     kb = rows(3, 1, 64, 5)
