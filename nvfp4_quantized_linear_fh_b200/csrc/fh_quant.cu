@@ -23,9 +23,10 @@
 // to the largest finite value) of that FP32 product gives the exact code; the
 // multiply and the converter are monotone, so agreement at every boundary
 // means agreement on every BF16 input.  Blocks whose scale code failed the
-// check (exact ties at non-power-of-two scales, typically) take the exact
-// threshold-compare path.  The block scale takes a converter candidate and
-// corrects it against the exact scale thresholds.
+// check (exact ties at non-power-of-two scales, typically) take a multiplier of
+// two parts, checked in the same way, or the exact threshold-compare path.  The
+// block scale takes a converter candidate and corrects it against the exact
+// scale thresholds.
 //
 // Memory: a producer warp streams units of x into a 96 KB ring of
 // shared-memory stages; each of 512 consumer threads quantizes one 16-element
