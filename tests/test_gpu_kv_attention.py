@@ -247,6 +247,16 @@ def test_many_requests(n, Hq, Hk, d):
     c.check(causal=False, window=9)
 
 
+@pytest.mark.parametrize("n", [63, 64, 65])
+def test_requests_of_equal_and_of_mixed_lengths(n):
+    """Many rows: the requests' tiles are put in order of their keys, up to 64 requests; lengths come in pairs."""
+    i = np.arange(n)
+    lens, n_q = 20 + 30 * (i // 2 * 7 % 11), np.where(i % 9 == 4, 0, 1 + i * 5 % 90)
+    c = Case(lens, n_q, 6, 2, 64, 16, seed=n, gap=2).poison_tails().device()
+    c.check()
+    c.check(window=33)
+
+
 @pytest.mark.parametrize("lens,n_q,Hq,Hk,d", [([70, 9], [1, 2], 72, 1, 64), ([45, 200], [3, 1], 130, 2, 128),
                                               ([5], [1], 4096, 4096, 64), ([40], [1], 1000, 1000, 128)])
 def test_many_heads(lens, n_q, Hq, Hk, d):
