@@ -24,8 +24,9 @@ namespace fh {
 
 struct __align__(16) QuantTable {
   // [c][j<7]: smallest |x| (BF16 bits) whose exact magnitude code is >= j+1 at scale code c.
-  // [c][7]: BF16 bits of the multiplier's rest, 1 / (S_c * s_g) less the FP32 in sc[c].x, where the
-  //      converter is exact on x times the two but not on x times the first; else +Inf bits.
+  // [c][7]: BF16 bits of the multiplier's rest, 1 / (S_c * s_g) less the FP32 in sc[c].x (rounded down
+  //      then: the rest is > 0), where the converter is exact on x times the two but not on x times
+  //      one FP32; else +Inf bits.
   uint16_t code_thr[128][8];
   // Per scale code c, everything one block needs in one 8-byte load:
   //   x: the FP32 bits of 1 / (S_c * s_g), the multiplier of the converter path
@@ -79,7 +80,8 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(float inv, uint32_t w0, uint32_t 
 }
 
 // The same with a multiplier of two parts: x * inv + x * lo, rounded once (and
-// x * lo before it, by 2^-24 of 2^-24).
+// x * lo before it, by 2^-24 of 2^-23).  lo > 0, or -0 would lose its sign:
+// (-0) inv + (-0) lo is +0 for a negative lo.
 __device__ __forceinline__ uint32_t cvt_e2m1x8_rest(float inv, float lo, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
   uint32_t r;
   asm("{\n\t.reg .b64 s, r, a0, a1, a2, a3, b0, b1, b2, b3;\n\t.reg .f32 l0, h0, l1, h1, l2, h2, l3, h3;\n\t.reg .b8 t0, t1, t2, t3;\n\t"

@@ -145,7 +145,8 @@ void build_table(float sg_f, QuantTable* t) {
     inv[c] = (c == 0 || c == 127) ? 0.0f : (float)(1.0 / (e4m3_magnitude(c) * sg));
   }
   // Converter path check at both sides of every boundary and at the ends of the
-  // BF16 range.  Negative inputs give the same magnitude with the sign bit set.
+  // BF16 range, in both signs: a negative input, -0 included, gives the same
+  // magnitude with the sign bit set.
   // When the FP32 product of a boundary value lands on a midpoint the nearest
   // multiplier fails the check; a neighbouring FP32 multiplier usually passes,
   // so up to two on each side are tried before the code falls back to a
@@ -160,8 +161,10 @@ void build_table(float sg_f, QuantTable* t) {
       bool ok = true;
       auto probe = [&](uint32_t a) {
         const float x = bf16_bits_value(a);
-        const float y = rest == 0.0f ? x * inv : fmaf(x, inv, x * rest);  // as the kernel's FP32 operations
-        ok = ok && converter_e2m1(y) == exact_mag(a);
+        // As the kernel's FP32 operations.
+        const float y = rest == 0.0f ? x * inv : fmaf(x, inv, x * rest);
+        const float n = rest == 0.0f ? -x * inv : fmaf(-x, inv, -x * rest);
+        ok = ok && converter_e2m1(y) == exact_mag(a) && n == -y && signbit(n);
       };
       probe(0);
       probe(0x7F7Fu);
@@ -184,13 +187,20 @@ void build_table(float sg_f, QuantTable* t) {
         break;
       }
     }
-    // Else the multiplier in two parts, the second one a BF16.
+    // Else the multiplier in two parts: the largest FP32 that is not above it, and a
+    // BF16 for the rest.  The rest is not negative, so that both products of a -0
+    // are -0 and their sum is too.
     if (!fast_ok[c] && c != 0 && isfinite(inv0)) {
-      const float rest = (float)(1.0 / (e4m3_magnitude(c) * sg) - (double)inv0);
+      const double exact = 1.0 / (e4m3_magnitude(c) * sg);
+      const float below = (double)inv0 > exact ? dn1 : inv0;
+      const float rest = (float)(exact - (double)below);
       uint32_t bits;
       memcpy(&bits, &rest, 4);
-      bits &= 0xFFFF0000u;  // cut: 2^-7 of what is 2^-24 of the multiplier
-      if (bits != 0 && passes(inv0, bf16_bits_value(bits >> 16))) t->code_thr[c][7] = (uint16_t)(bits >> 16);
+      bits &= 0xFFFF0000u;  // cut: 2^-7 of what is 2^-23 of the multiplier
+      if (bits != 0 && passes(below, bf16_bits_value(bits >> 16))) {
+        inv[c] = below;
+        t->code_thr[c][7] = (uint16_t)(bits >> 16);
+      }
     }
   }
   // The packed per-code entries the kernels read.
