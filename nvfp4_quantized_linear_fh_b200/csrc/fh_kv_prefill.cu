@@ -1022,7 +1022,7 @@ cudaError_t read_and_clear_kv_error(unsigned int* bits) {
   unsigned int v = 0, zero = 0;
   cudaError_t e = cudaMemcpyFromSymbol(&v, g_kv_error, sizeof v);
   if (e != cudaSuccess) return e;
-  e = cudaMemcpyToSymbol(g_kv_error, &zero, sizeof zero);
+  if (v != 0) e = cudaMemcpyToSymbol(g_kv_error, &zero, sizeof zero);  // (clearing takes as long as reading)
   *bits = v;
   return e;
 }

@@ -856,7 +856,7 @@ cudaError_t read_and_clear_quant_error(unsigned int* bits) {
   unsigned int v = 0, zero = 0;
   cudaError_t e = cudaMemcpyFromSymbol(&v, g_quant_error, sizeof v);
   if (e != cudaSuccess) return e;
-  e = cudaMemcpyToSymbol(g_quant_error, &zero, sizeof zero);
+  if (v != 0) e = cudaMemcpyToSymbol(g_quant_error, &zero, sizeof zero);  // (clearing takes as long as reading)
   *bits = v;
   return e;
 }
