@@ -215,11 +215,12 @@ __global__ void __launch_bounds__(kPagesThreads, 1) kv_pages_kernel(const PagesP
     const int at = count + n_given - 1 - i;
     return at >= count ? given_page(at - count) : p.free_pages[at];
   };
-  for (int i = gt; i < n_taken; i += all) {
-    const int b = owner_of(taken, 0, n, i);
-    p.table[(int64_t)b * p.max_pages + pages_of(held_s[b]) + (i - taken[b])] = taken_page(i);
+  // (64-bit: the totals may be 2^31 - 1, and the last step goes past them.)
+  for (int64_t i = gt; i < n_taken; i += all) {
+    const int b = owner_of(taken, 0, n, (int)i);
+    p.table[(int64_t)b * p.max_pages + pages_of(held_s[b]) + ((int)i - taken[b])] = taken_page((int)i);
   }
-  for (int f = gt; f < n_given; f += all) p.free_pages[(int64_t)count + f] = given_page(f);
+  for (int64_t f = gt; f < n_given; f += all) p.free_pages[count + f] = given_page((int)f);
 
   if (with_slots)
     write_slots(p, starts, n_rows, gt >> 5, all / 32, [&](int b) { return held_s[b]; },

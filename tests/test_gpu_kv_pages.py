@@ -179,3 +179,32 @@ def test_captured_steps_with_many_slots():
         for r, g in zip(ref[1:], (table, free, count, held, qs, slots)):
             np.testing.assert_array_equal(g.cpu().numpy().reshape(np.shape(r)), r)
         state = [ref[4], ref[1], ref[2], ref[3]]
+
+
+def test_as_many_pages_as_the_sizes_allow():
+    """2^31 - 1 pages of one token taken in one step and given back in the next: the last threads' next entry would be
+    past 32 bits."""
+    m = fh()
+    n, half = 2 ** 31 - 1, 2 ** 30
+    held, target = i32([0, 0]), i32([half, half - 1])
+    table = torch.full((2, half), -7, dtype=torch.int32, device="cuda")
+    free = torch.arange(n, dtype=torch.int32, device="cuda")
+    count, starts, status = i32([n]), i32([0, 0, 0]), i32([9])
+    slots = torch.zeros(n, dtype=torch.int64, device="cuda")
+
+    def down(t):
+        """t[i] == n - 1 - i throughout."""
+        step = 1 << 28
+        return all(torch.equal(t[a:a + step], torch.arange(n - 1 - a, n - 1 - min(a + step, n), -1, dtype=t.dtype,
+                                                           device="cuda")) for a in range(0, n, step))
+
+    def step():
+        m.fh_kv_pages_update(held, target, table, free, count, count, held, starts, slots, status, 1)
+        return int(status), int(count), held.tolist(), starts.tolist()
+    assert step() == (0, 0, [half, half - 1], [0, half, n])
+    assert down(table.view(-1)[:n]) and int(table[1, -1]) == -7 and down(slots)
+    assert int(free[0]) == 0 and int(free[-1]) == n - 1
+    target.zero_()
+    assert step() == (0, n, [0, 0], [0, 0, 0])
+    assert down(free) and down(table.view(-1)[:n])
+    assert int(slots.max()) == -1 and int(slots.min()) == -1
