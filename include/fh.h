@@ -485,8 +485,8 @@ int fh_kv_cache_read(const fh_kv_cache* cache, const int64_t* slots_dev, int64_t
  * aligned, zero before the first call that uses it (cudaMemsetAsync); every call
  * leaves its counters zero again.  Calls that may overlap on the GPU need
  * workspaces of their own.
- * q_heads a multiple of kv_heads, total_q * q_heads < 2^31; ldq, ldo >= q_heads *
- * head_dim, multiples of 8; q, out 16-byte aligned; sm_scale finite; 0 <= window
+ * q_heads a multiple of kv_heads, total_q * q_heads < 2^31; 0 <= batch < 2^31 - 1;
+ * ldq, ldo >= q_heads * head_dim, multiples of 8; q, out 16-byte aligned; sm_scale finite; 0 <= window
  * < 2^31; 0 < max_pages, max_pages * page_size <= 2^30; a cache of
  * at least one page.  total_q == 0 or batch == 0 enqueues nothing.
  * A bounded wait that expires inside the kernel for many rows sets the device

@@ -70,6 +70,13 @@ __device__ __forceinline__ Request load_request(const AttnParams& p, int b) {
   return r;
 }
 
+// Thread i's share of the requests where `threads` share them: [x, y).  (Unsigned:
+// with batch < 2^31 - 1, i per < 2^31 and i per + per < 2^32.)
+__device__ __forceinline__ int2 share_of_requests(const AttnParams& p, uint32_t i, uint32_t threads) {
+  const uint32_t n = (uint32_t)p.batch, per = (n - 1) / threads + 1, from = min(n, i * per);
+  return make_int2((int)from, (int)min(n, from + per));
+}
+
 // The cached tokens [lo, hi) that query i of a request sees.
 __device__ __forceinline__ int2 seen_by(const AttnParams& p, const Request& r, int i) {
   const int64_t pos = (int64_t)r.len - r.n_q + i;

@@ -162,8 +162,8 @@ __global__ void __launch_bounds__(kThreads, 3) kv_decode_kernel(const __grid_con
 
   // --- this CTA's piece of the line ------------------------------------------------
   Walk w;
-  const int per = (p.batch + kThreads - 1) / kThreads;
-  const int rb0 = min(p.batch, tid * per), rb1 = min(p.batch, rb0 + per);
+  const int2 share = share_of_requests(p, tid, kThreads);
+  const int rb0 = share.x, rb1 = share.y;
   long long mine = 0;
   for (int b = rb0; b < rb1; ++b) {
     w.b = b;

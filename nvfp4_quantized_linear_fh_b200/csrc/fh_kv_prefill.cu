@@ -364,8 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (under a causal mask the longest) first ----------------------------------------
   constexpr int kCtaRows = kRows * kTiles;
   auto tiles_of = [&](const Request& r) { return (int)(((int64_t)r.n_q * p.group + kCtaRows - 1) / kCtaRows); };
-  const int per = (p.batch + kThreads - 1) / kThreads;
-  const int rb0 = min(p.batch, tid * per), rb1 = min(p.batch, rb0 + per);
+  const int2 share = share_of_requests(p, tid, kThreads);
+  const int rb0 = share.x, rb1 = share.y;
   long long mine = 0;  // (q_starts that decrease can name more rows than there are)
   Request rq;
   for (int b = rb0; b < rb1; ++b) {
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (place >= first && place < first + mine) {
     long long rest = first + mine - 1 - place;
     for (int b = rb0; b < rb1; ++b) {
-      if (per > 1) rq = load_request(p, b);
+      if (rb1 - rb0 > 1) rq = load_request(p, b);
       const int n = tiles_of(rq);
       if (rest < n) {
         job_s[0] = b;

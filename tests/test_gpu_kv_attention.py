@@ -595,3 +595,19 @@ def test_a_call_waits_for_its_own_and_for_other_streams(graph, kernel):
         torch.cuda.synchronize()
         for a, b in zip(outs, want):
             assert torch.equal(a, b)
+
+
+def test_as_many_requests_as_a_call_may_have(kernel):
+    """2^31 - 2 requests, all but the eighth and the last without a query: threads' shares of them end near 2^31."""
+    m = fh()
+    c = Case([5, 20], [1, 2], 4, 2, 128, 32, seed=2, extra_pages=0, gap=1).device()
+    n = 2 ** 31 - 2
+    lens, table = (torch.zeros(n, dtype=torch.int32, device="cuda") for _ in range(2))
+    starts = torch.ones(n + 1, dtype=torch.int32, device="cuda")
+    starts[:8], starts[n] = 0, 3
+    for at, b in ((7, 0), (n - 1, 1)):
+        lens[at], table[at] = int(c.lens[b]), int(c.table[b, 0])
+    c.t_lens, c.t_starts, c.t_table = lens, starts, table.view(n, 1)
+    c.ws = m.empty_kv_attention_workspace(c.T, n, c.Hq, c.Hk, c.d)
+    sm = float(np.float32(0.09))
+    compare(*c.run(sm, causal=True), *c.reference(sm, True, 0))
