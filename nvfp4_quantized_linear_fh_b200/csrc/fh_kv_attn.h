@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "fh_internal.h"
+#include "fh_kv.cuh"
 
 namespace fh {
 namespace kv {
@@ -27,7 +28,11 @@ struct AttnParams {
   int page_shift, num_pages;
   int causal, window;
   int stall;        // test hook: the tile kernel's first CTA stops its products after two key tiles
-  float qk_scale;  // sm_scale * log2(e) * k_gscale: scores in units of log2
+  // sm_scale * log2(e) * k_gscale = qk_scale * 2^qk_exp, for scores in units of log2;
+  // 0.5 <= |qk_scale| <= 1, or both are 0: the product may be outside FP32 where the
+  // scores are not.
+  float qk_scale;
+  int qk_exp;
   float v_gscale;
   // Workspace: partial results of key ranges split over CTAs, and their counters.
   float* part_o;        // [slots][rows][d], not normalised
@@ -68,6 +73,12 @@ __device__ __forceinline__ Request load_request(const AttnParams& p, int b) {
   r.lo = 0;
   if (p.window > 0) r.lo = (int)min((int64_t)r.hi, max((int64_t)0, (int64_t)r.len - r.n_q - p.window + 1));
   return r;
+}
+
+// What turns a row's sums into scores in units of log2, its query having been scaled
+// by 2^e.  Never 0: a hidden score of -inf stays -inf times it.
+__device__ __forceinline__ float score_factor(const AttnParams& p, int e) {
+  return fmaxf(fabsf(p.qk_scale) * pow2(min(max(p.qk_exp - e, -126), 127)), 1.17549435e-38f);
 }
 
 // Thread i's share of the requests where `threads` share them: [x, y).  (Unsigned:

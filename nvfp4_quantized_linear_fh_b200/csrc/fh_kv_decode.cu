@@ -338,8 +338,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_decode_kernel(const __grid_con
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int col = 2 * t + c;
-      // Never 0: a hidden score of -inf stays -inf times it.
-      factor[c] = fmaxf(fabsf(p.qk_scale) * pow2(-__shfl_sync(0xFFFFFFFFu, e, 4 * col)), 1.17549435e-38f);
+      factor[c] = score_factor(p, __shfl_sync(0xFFFFFFFFu, e, 4 * col));
       const int2 s = col < n_rows ? seen_by(p, rq, (int)query_of_row(p, (uint32_t)seg_tile * R + col)) : make_int2(0, rq.hi);
       lo_q[c] = s.x;
       hi_q[c] = s.y;

@@ -498,8 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int e = query_exponent(max(amax & 0x7FFFu, (amax >> 16) & 0x7FFFu));
       // A negative scale goes to the query, so that larger scores are larger sums.
       const float up = p.qk_scale < 0.0f ? -pow2(e) : pow2(e);
-      // Never 0: a hidden score of -inf stays -inf times it.
-      factor = fmaxf(fabsf(p.qk_scale) * pow2(-e), 1.17549435e-38f);
+      factor = score_factor(p, e);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};

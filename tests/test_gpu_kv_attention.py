@@ -611,3 +611,13 @@ def test_as_many_requests_as_a_call_may_have(kernel):
     c.ws = m.empty_kv_attention_workspace(c.T, n, c.Hq, c.Hk, c.d)
     sm = float(np.float32(0.09))
     compare(*c.run(sm, causal=True), *c.reference(sm, True, 0))
+
+
+@pytest.mark.parametrize("n_q", [1, 33])
+@pytest.mark.parametrize("sm_scale,k_gscale,q_scale", [(1e19, 1e20, 3e-40), (-1e25, 1e13, 3e-39), (1e-20, 3e-21, 1e37),
+                                                       (1e-30, 1e-20, 1e36)])
+def test_products_of_scales_outside_fp32(n_q, sm_scale, k_gscale, q_scale):
+    """sm_scale times the keys' scale is beyond FP32, or has few bits there, while the scores are ordinary."""
+    c = Case([333, 64], [n_q, n_q], 4, 1, 128, 16, seed=6, q_scale=q_scale)
+    c.gs = (float(np.float32(k_gscale)), c.gs[1])
+    c.device().check(sm_scale=float(np.float32(sm_scale)))
