@@ -41,7 +41,9 @@ cudaError_t launch_kv_attention(const fh_kv_cache& c, const KvAttnCall& call, co
   const char* stall = getenv("FH_KV_TEST_STALL");  // read at each launch
   p.stall = stall != nullptr && stall[0] == '1' ? 1 : 0;
   p.qk_scale = (float)frexp((double)call.sm_scale * 1.4426950408889634 * (double)c.k_gscale, &p.qk_exp);
-  p.v_gscale = c.v_gscale;
+  int v_exp;
+  p.v_scale = 2.0f * frexpf(c.v_gscale, &v_exp);
+  p.v_unit = ldexpf(1.0f, v_exp - 1);
   p.part_o = nullptr;
   p.part_ml = nullptr;
   p.count = nullptr;

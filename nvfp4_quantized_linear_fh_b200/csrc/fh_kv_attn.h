@@ -33,7 +33,10 @@ struct AttnParams {
   // scores are not.
   float qk_scale;
   int qk_exp;
-  float v_gscale;
+  // v_gscale = v_scale * v_unit, 1 <= v_scale < 2 and v_unit a power of two: outputs are
+  // divided by the softmax's denominator in units of v_unit, since v_gscale / it may be
+  // below FP32's normal range where the outputs are not.
+  float v_scale, v_unit;
   // Workspace: partial results of key ranges split over CTAs, and their counters.
   float* part_o;        // [slots][rows][d], not normalised
   float2* part_ml;      // [slots][rows]: running maximum (log2 units) and sum

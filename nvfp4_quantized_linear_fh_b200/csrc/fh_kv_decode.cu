@@ -571,8 +571,9 @@ __global__ void __launch_bounds__(kThreads, 3) kv_decode_kernel(const __grid_con
       const uint32_t rr = (uint32_t)seg_tile * R + row, ti = query_of_row(p, rr);
       const int64_t tok = rq.row0 + (int64_t)ti;
       const int head = seg_head * p.group + (int)(rr - ti * p.group);
-      const float inv = ll > 0.0f ? p.v_gscale / ll : (ll == 0.0f ? 0.0f : ll);  // a NaN stays one
-      uint2 v = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+      const float inv = ll > 0.0f ? p.v_scale / ll : (ll == 0.0f ? 0.0f : ll);  // a NaN stays one
+      const float unit = p.v_unit;
+      uint2 v = make_uint2(pack_bf16x2(o.x * inv * unit, o.y * inv * unit), pack_bf16x2(o.z * inv * unit, o.w * inv * unit));
       *reinterpret_cast<uint2*>(p.out + tok * p.ldo + (int64_t)head * D + d) = v;
       if (d == 0 && p.lse != nullptr)
         p.lse[tok * p.q_heads + head] = ll == 0.0f ? -INFINITY : (mm - kHead + log2f(ll)) * 0.6931471805599453f;

@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (ok) {
-        const float inv = l > 0.0f ? p.v_gscale / l : (l == 0.0f ? 0.0f : l);
+        const float inv = l > 0.0f ? p.v_scale / l : (l == 0.0f ? 0.0f : l);
         // Through shared memory (this warp's part of its Q tile, which the products
         // are done with), so that the stores cover whole lines.
         uint8_t* stage = smem + C::kOffQ + t * C::kOperand + (warp & 3) * (32 * D * 2);
@@ -695,7 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              w[k] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * k]) * inv, __uint_as_float(v[8 * i + 2 * k + 1]) * inv);
+              w[k] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * k]) * inv * p.v_unit,
+                                 __uint_as_float(v[8 * i + 2 * k + 1]) * inv * p.v_unit);
             *reinterpret_cast<uint4*>(stage + lane * (2 * D) + (((4 * c + i) ^ (lane & 7)) * 16)) =
                 make_uint4(w[0], w[1], w[2], w[3]);
           }

@@ -621,3 +621,17 @@ def test_products_of_scales_outside_fp32(n_q, sm_scale, k_gscale, q_scale):
     c = Case([333, 64], [n_q, n_q], 4, 1, 128, 16, seed=6, q_scale=q_scale)
     c.gs = (float(np.float32(k_gscale)), c.gs[1])
     c.device().check(sm_scale=float(np.float32(sm_scale)))
+
+
+@pytest.mark.parametrize("n_q", [1, 33])
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_least_scales_of_values(d, n_q):
+    """A scale of the values of which FP32 keeps few bits once it is divided by the softmax's denominator: 4000 equal
+    keys, and values of 2688 times the scale."""
+    c = Case([4000, 90], [n_q, n_q], 2, 1, d, 64, seed=4)
+    c.arrays[0][:] = 0x22
+    c.arrays[1][:] = 0x38
+    c.arrays[2][:] = 0x77
+    c.arrays[3][:] = 0x7E
+    c.gs = (c.gs[0], float(np.float32(1e-39)))
+    c.device().check(causal=False)
