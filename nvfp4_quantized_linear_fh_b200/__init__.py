@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from operator import index as _index
 
 import torch
 
@@ -534,7 +535,7 @@ def fh_kv_pages_update(held: torch.Tensor, target: torch.Tensor, block_table: to
             or status.numel() != 1):
         raise ValueError("shape mismatch: held, target, lens [batch], q_starts [batch + 1], block_table [batch, "
                          "max_pages], free_count, free_count_out, status [1]")
-    _check(_lib.fh_kv_pages_update(held.data_ptr(), target.data_ptr(), n, page_size, block_table.data_ptr(),
+    _check(_lib.fh_kv_pages_update(held.data_ptr(), target.data_ptr(), n, _index(page_size), block_table.data_ptr(),
                                    block_table.shape[1], free_pages.data_ptr(), free_pages.numel(),
                                    free_count.data_ptr(), free_count_out.data_ptr(), lens.data_ptr(),
                                    q_starts.data_ptr(), slots.data_ptr(), slots.numel(), status.data_ptr(),
@@ -632,9 +633,9 @@ def fh_kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
             raise ValueError("lse must be [total_q, q_heads]")
     max_pages = block_table.shape[1]
     _check(_lib.fh_kv_attention(cache._ref, q.data_ptr(), total_q, heads, _row_stride(q, "q"), block_table.data_ptr(),
-                                max_pages, lens.data_ptr(), q_starts.data_ptr(), n, sm_scale, 1 if causal else 0,
-                                window, total_q if max_q is None else max_q,
-                                max_pages * cache.page_size if max_kv is None else max_kv, out.data_ptr(),
+                                max_pages, lens.data_ptr(), q_starts.data_ptr(), n, float(sm_scale), 1 if causal else 0,
+                                _index(window), total_q if max_q is None else _index(max_q),
+                                max_pages * cache.page_size if max_kv is None else _index(max_kv), out.data_ptr(),
                                 _row_stride(out, "out"), None if lse is None else lse.data_ptr(),
                                 workspace.data_ptr(), workspace.numel(), _raw_stream(stream, index)))
 

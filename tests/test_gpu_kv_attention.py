@@ -635,3 +635,16 @@ def test_the_least_scales_of_values(d, n_q):
     c.arrays[3][:] = 0x7E
     c.gs = (c.gs[0], float(np.float32(1e-39)))
     c.device().check(causal=False)
+
+
+def test_numbers_of_numpy():
+    """Scalars as numpy has them, where the other calls take them too."""
+    c = Case([90, 40], [2, 1], 4, 2, 64, 16, seed=3).device()
+    sm = np.float32(0.125)
+    ref = c.reference(float(sm), True, 33)
+    compare(*c.run(sm, causal=np.bool_(True), window=np.int32(33), max_q=np.int64(2), max_kv=np.int64(90)), *ref)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    one, status, slots = i32([0]), i32([9]), torch.zeros(4, dtype=torch.int64, device="cuda")
+    c.m.fh_kv_pages_update(one, i32([3]), i32([[-1, -1]]), i32([5]), i32([1]), i32([0]), i32([0]), i32([0, 0]), slots,
+                           status, np.int64(16))
+    assert int(status) == 0 and slots.tolist() == [80, 81, 82, -1]
