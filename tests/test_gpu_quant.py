@@ -162,3 +162,24 @@ def test_gelu_against_oracle():
 
 def test_device_status_clean():
     fh().fh_device_status()
+
+
+def _places_of(home, n):
+    """n global scales whose decision tables are looked for from the same of 512 places on."""
+    bits = np.arange(0x3A000000, 0x3D000000, 4099, dtype=np.uint64)
+    bits = bits[((bits * 0x9E3779B1) & 0xFFFFFFFF) >> 23 == home][:n].astype(np.uint32)
+    assert len(bits) == n
+    return [float(s) for s in bits.view(np.float32)]
+
+
+@pytest.mark.parametrize("home", [3, 507])
+def test_scales_that_share_a_place_in_the_table_cache(home):
+    """Eight tables are kept from a place on, and a ninth scale takes the first one's: twenty in turns, three times, so
+    that tables are found again, given up and built anew; at the last places the search goes on from the first."""
+    x = S.random_bf16(("gpu", "places"), (4, 64), 0.05)
+    for _ in range(3):
+        for sg in _places_of(home, 20) + _places_of((home + 7) % 512, 3):
+            check_quantize(x, sg, ROW)
+    first = _places_of(home, 2)
+    for i in range(6):
+        check_quantize(x, first[i % 2], TILED)
