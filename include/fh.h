@@ -416,6 +416,7 @@ enum {
  *   - slots[q_starts[b] + i] = the slot of request b's token held[b] + i, for
  *     fh_kv_cache_write; -1 from q_starts[batch] on, up to slot_capacity.
  *   - *free_count_out = the stack's new count; *status = 0.
+ * A page has one holder: one that two rows name is given back by both.
  * All or nothing: if the step cannot be served, *status has the bits that say
  * why, slots are all -1, q_starts all 0, lens = held, *free_count_out =
  * *free_count, and block_table and free_pages are as they were.
@@ -476,7 +477,8 @@ int fh_kv_cache_read(const fh_kv_cache* cache, const int64_t* slots_dev, int64_t
  * page_size, and rows to total_q.
  * max_q and max_kv are the caller's upper bounds of a request's queries and of
  * lens (total_q and max_pages * page_size will do): they choose the kernel and
- * its grid; with wrong ones the call is slower, never wrong.
+ * its grid; with wrong ones the call is slower, never wrong.  One kernel takes the
+ * whole call: a step of single tokens and a long prompt is faster as two calls.
  * Scores, maxima, sums and outputs are FP32; the products' operands are FP16:
  * code * scale is exact there, so is a BF16 query row scaled by a power of two,
  * and probabilities are rounded to 2^-11.  Deterministic for given arguments

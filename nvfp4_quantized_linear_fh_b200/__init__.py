@@ -489,7 +489,8 @@ def empty_kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int,
 
 
 # The cache's calls run once a layer and token, some for a few microseconds: their checks are written for few
-# attribute reads (a device is compared by its index, the stream is read as the raw handle).
+# attribute reads.  A device is compared by its index (0.06 us; by its type 0.21) and the stream is read as the raw
+# handle (0.07 us; 1.3 through torch.cuda.current_stream, 3.4 by _stream).
 
 def _need_all(index, dtype, names, *tensors):
     """Contiguous tensors of one dtype on CUDA device `index`."""

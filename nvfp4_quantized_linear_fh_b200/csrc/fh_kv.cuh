@@ -84,7 +84,8 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // log2 of the power of two that brings a query row whose largest BF16 magnitude
 // (bits) is `amax` to [2^13, 2^14): scaled so, the row goes to FP16 without a
 // rounding that matters (elements 2^-27 of the largest and more stay exact, the
-// others are off by at most 2^-39 of it), and its products with keys of up to
+// others are off by at most half an FP16 subnormal's step, 2^-25, which is 2^-38
+// of the largest), and its products with keys of up to
 // 2688 stay far inside FP32.  0 for a zero or non-finite row.
 __device__ __forceinline__ int query_exponent(uint32_t amax) {
   const int e = (int)(amax >> 7);

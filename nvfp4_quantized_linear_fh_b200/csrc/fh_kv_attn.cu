@@ -52,7 +52,10 @@ cudaError_t launch_kv_attention(const fh_kv_cache& c, const KvAttnCall& call, co
   // 256.  Measured with both, in us (few / tiles): 32 rows of 16 requests of up to
   // 4000 tokens, 8 KV heads, 52 / 72; 64 rows of them 67 / 72; 64 rows of 64
   // requests of up to 1000, 92 / 78; 48 rows of one of 30000, 21 KV heads,
-  // 124 / 91; 64 rows of one of 30000, one KV head, 30 / 78.
+  // 124 / 91; 64 rows of one of 30000, one KV head, 30 / 78.  The choice is the whole
+  // call's, and max_q is all that it knows of the requests' rows: 63 single tokens and
+  // a prompt's 512 over up to 8192 tokens, 32 heads over 8, take 602 / 317 as one call
+  // (here the estimate is wrong) and 87 + 81 as two.
   int64_t max_kv = shape.max_kv;
   if (p.window > 0 && max_kv > (int64_t)p.window + shape.max_q) max_kv = (int64_t)p.window + shape.max_q;
   bool few = shape.max_q * p.group <= kFewRows || kv_attn_split_cost(shape, max_kv) < kv_attn_tiles_cost(shape, max_kv);

@@ -31,8 +31,8 @@ using namespace nvfp4;
 
 constexpr int kKvThreads = 256;
 // Blocks of a thread in flight.  32768 tokens x 21 heads x 128: write 87 us
-// with four in 64 registers (four CTAs an SM), 100 in 80 registers, 91 with
-// two; read 73 with two, 79 with four.
+// with four in 64 registers (four CTAs an SM; 100 bytes a thread are spilled),
+// 100 in 80 registers, 91 with two; read 73 with two, 79 with four.
 constexpr int kWriteBlocks = 4, kReadBlocks = 2;
 
 // One of keys and values.

@@ -3,9 +3,12 @@
 //
 //   out[t, h] = sum_j p_j v[j, h / G],  p = softmax_j(sm_scale q[t, h] . k[j, h / G])
 //
-// with k, v = code * S * s_g read straight from the cache.  The call is bound by
-// HBM: at d = 128 a cached token of one KV head is 144 bytes, shared by the G
-// query heads of its group.
+// with k, v = code * S * s_g read straight from the cache.  What a call cannot do
+// without is reading it: at d = 128 a cached token of one KV head is 144 bytes,
+// shared by the G query heads of its group.  64 requests of up to 8192 tokens, 8
+// KV heads: 88.4 us, 59 % of the HBM rate.  No one unit is full (issue slots 57 %,
+// ALU 49 %, tensor pipe 21 %): three warps a scheduler wait for their own
+// conversions and products.
 //
 // Work split.  A tile is eight query rows (row = token * G + head in group)
 // of one request and one KV head; its keys are cut into units of 128 tokens.

@@ -68,7 +68,12 @@ constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups: two warps of
 constexpr int kSoftRegs = 176, kOtherRegs = 80;
 constexpr int kLive = 4;       // ring of the key tiles' page masks
 constexpr int kMaxPieces = 8;  // of a row tile's keys
-constexpr int kSorted = 64;    // requests that are put in order, each by a thread that looks at all others
+// Requests that are put in order, each by a thread that looks at all others.  More
+// take the batch's order, last to first; put in order as well (128 here), in us: 66 of
+// 64 .. 4000 tokens, 8 heads over 2, 222, and 233 in the batch's order (219 .. 238 by
+// that order); 100 of up to 2000, d = 64, 141 and 149 (137 .. 156); 128 of 200 .. 1500,
+// 118.5 and 122 (114.5 .. 125).
+constexpr int kSorted = 64;
 constexpr int kMaxPieceCtas = 320;  // workspace bound: a partial result each
 constexpr float kRaise = 8.0f;
 constexpr float kHead = 6.0f;
