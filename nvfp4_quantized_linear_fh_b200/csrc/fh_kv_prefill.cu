@@ -596,6 +596,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float off = m == -INFINITY ? 0.0f : kHead - m;
+        // A step's weights are added up by themselves: many that are each below the last
+        // place of the row's sum count by what they are together.
+        float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t h[16];
@@ -604,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])),
                                         make_float2(factor, factor), make_float2(off, off));
             const float2 w = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-            sum = __fadd2_rn(sum, w);
+            part = __fadd2_rn(part, w);
             h[i] = pack_f16x2(w.x, w.y);
           }
           tmem_store_16(ts + 16 * c, h);
@@ -614,6 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             warp_arrive(!kAhead && t == 0 && c == 1 ? pfirst(j) : pfull(t, c >> 1, j), lane);
           }
         }
+        sum = __fadd2_rn(sum, part);
       }
       l = sum.x + sum.y;
       // (Without keys no product has waited for the other warps' queries, over which the output is staged.)

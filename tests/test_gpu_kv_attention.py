@@ -2,6 +2,7 @@
 the bound of the kernels' roundings (tests/_kv_ref.py), over head layouts,
 lengths, pages, masks and strides; then the whole run of a cache's calls."""
 import contextlib
+import math
 import os
 
 import numpy as np
@@ -648,3 +649,30 @@ def test_numbers_of_numpy():
     c.m.fh_kv_pages_update(one, i32([3]), i32([[-1, -1]]), i32([5]), i32([1]), i32([0]), i32([0]), i32([0, 0]), slots,
                            status, np.int64(16))
     assert int(status) == 0 and slots.tolist() == [80, 81, 82, -1]
+
+
+@pytest.mark.parametrize("d,L,n_q,log2w", [(64, 60000, 33, -23.86), (128, 60000, 33, -23.86), (64, 30000, 300, -24.6),
+                                           (128, 200000, 2, -23.7)])
+def test_many_small_weights_beside_a_large_one(d, L, n_q, log2w):
+    """A token that all queries look at, and tens of thousands whose weights are each about one unit in the last place
+    of its: they count by what they are together.
+
+    The bound: a sum of one addition a 64 keys and 64 within them, 2^-24 each; the scores, 0 and -log2w, are exact but
+    for three roundings and ex2's argument and result."""
+    c = Case([L], [n_q], 1, 1, d, 128, seed=5)
+    c.q[:] = S.to_bf16_bits(np.ones((c.T, 1, d)))
+    c.arrays[0][:] = 0x22       # ones
+    c.arrays[1][:] = 0          # times 0 ...
+    c.arrays[1][c.table[0, 3], 0, 7] = 0x38  # ... but for one token
+    c.arrays[2][:] = 0x22
+    c.arrays[3][:] = 0x38
+    c.gs = (1.0, c.gs[1])
+    c.device()
+    sm = float(np.float32(-log2w * math.log(2) / d))
+    s = sm * d
+    want = s + math.log1p((L - 1) * math.exp(-s))
+    tol = (L / 64 + 64) * 2.0 ** -24 + 2.0 ** -21 * (1 + want) + 4 * 2.0 ** -24 * s
+    for kernel in ("few", "tiles"):
+        with selected(kernel):
+            _, lse = c.run(sm, causal=False)
+        assert np.abs(lse - want).max() <= tol, (kernel, np.abs(lse - want).max(), tol)
